@@ -20,6 +20,10 @@
  *   lazy_alibi_prefill_attn  the prefill step for models with ALiBi position biases
  *   attn_column_scores   PyramidKV-style key scores of a prompt's last rows (tcgen05)
  *   attn_column_scores_lse  the same from row log-sum-exps the attention already produced
+ *   paged_kv_append_rope a decode batch's or prompts' new rows, keys and queries rotated on the way
+ *   paged_kv_create_q4   a cache held in 4 bits; paged_kv_append_rope, score_blocks, the selection and
+ *                        the three sparse_decode_attn calls work on it
+ *   paged_kv_unpack_q4   pages of a 4-bit cache back as bf16 pages
  *   score_blocks_dir, sparse_decode_attn_dir, retrieve_pages_dir  the same calls through a
  *                        two-level page directory (spkv_pagemap_* manages one)
  *
@@ -76,6 +80,7 @@ enum spkv_status {
 #define SPKV_DEVERR_ORDER 8u        /* selected list not strictly ascending, or duplicate resident id */
 #define SPKV_DEVERR_CAPACITY 16u    /* more missing pages than evictable slots */
 #define SPKV_DEVERR_TIMEOUT 32u     /* a bounded intra-CTA wait gave up (reported as SPKV_ETIMEOUT) */
+#define SPKV_DEVERR_POS 64u         /* rotary position outside the table of cos and sin */
 
 typedef struct spkv_cache* spkv_cache_t; /* opaque, library-owned */
 
@@ -129,6 +134,93 @@ int paged_kv_create(const spkv_desc* desc, void* stream, spkv_cache_t* out);
  * [NOSA] "Method 2: NOSI", kernel fusion; [NOSA] "Method 1", block-wise implementation. */
 int paged_kv_append(spkv_cache_t cache, const int32_t* phys_page, const int32_t* tok_in_page,
                     const void* k_new, const void* v_new, int n_rows, void* stream);
+
+/* A cache held in 4 bits.  Of 16 dims x of one token-head (one block) it holds
+ *   a = max |x|,  s = e4m3(a / (6 g)),  code = e2m1(x / (s g)),  value = code s g
+ * with the nearest representable scale and code (ties to even, saturating) and one fp32 factor g > 0
+ * for a kv head: 4.5 bits a value, 9216 bytes a page-head (bf16: 32768).  A block of zeros, or so small
+ * that s is 0, holds zeros; a block with a NaN holds NaN; infinities saturate.  g is the caller's
+ * calibration: with g = (largest magnitude of the head) / 2688 nothing saturates.
+ *   kv_pool : [n_kv_heads][n_phys_pages][9216] bytes, 16-byte aligned.  Inside a page-head, with t the
+ *             token and k the block of 16 dims (8 bytes of codes, dim 2i in the low nibble of byte i):
+ *     key codes    64 t + 8 k
+ *     value codes  4096 + 512 (t / 8) + 64 k + 8 (t % 8)
+ *     key scales   8192 + 16 (4 (t % 8) + k / 2) + 4 (t / 16) + 2 ((t / 8) % 2) + k % 2
+ *     value scales 8704 + 16 (4 k + (t % 8) / 2) + 4 (t / 16) + 2 ((t / 8) % 2) + t % 2
+ *   k_scale, v_scale : device fp32 [n_kv_heads], the factors g; read by every call, so they must not
+ *                      change while the pool holds rows written with them.  g in [2^-64, 2^64].
+ *   the other fields : as spkv_desc (ksum holds sums of the values that the cache holds); page_cnt may
+ *                      be given without ksum, for paged_kv_unpack_q4. */
+typedef struct {
+  int32_t n_kv_heads;
+  int32_t head_dim;     /* must be 128 */
+  int32_t page_tokens;  /* must be 64 */
+  int32_t subblock;     /* must be 16 */
+  int64_t n_phys_pages;
+  void* kv_pool;
+  const float* k_scale;
+  const float* v_scale;
+  void* ksum;
+  int32_t* page_cnt;
+  int32_t max_units;
+  int32_t ksum_bf16;
+} spkv_desc_q4;
+
+/* paged_kv_create for a 4-bit cache.  On the handle work paged_kv_append_rope, paged_kv_unpack_q4,
+ * score_blocks(_dir), select_topk, resident_setdiff, lru_bucket_update, select_resident_update and
+ * sparse_decode_attn, _slots, _dir, with the arguments they have for a bf16 handle; the other calls,
+ * which read or write bf16 pages, return SPKV_EUNSUPPORTED (paged_kv_unpack_q4 gives them such pages). */
+int paged_kv_create_q4(const spkv_desc_q4* desc, void* stream, spkv_cache_t* out);
+
+/* Rotary positions of paged_kv_append_rope.
+ *   cos_sin   : device fp32 [n_pos][128], 16-byte aligned: at a position the cosines of the 64 pairs'
+ *               angles, then their sines (pairs (x_j, x_{j+64}); any scaling of the frequencies is the
+ *               table's)
+ *   n_axes    : 1 .. 4 axes of position (4: time, height, width and one more)
+ *   pair_axis : host uint8 [64], the axis whose position turns each pair; NULL with one axis
+ *   pos       : device int32 [n_rows][n_axes]; NULL (one axis only): a row's position in its context */
+typedef struct {
+  const float* cos_sin;
+  int64_t n_pos;
+  int32_t n_axes;
+  const uint8_t* pair_axis;
+  const int32_t* pos;
+} spkv_rope;
+
+/* Appends the new rows of B requests, with the rotation of their positions applied on the way: a decode
+ * step's one row a request, prompts of any lengths, or both in one call.  Rows row_first[b] ..
+ * row_first[b+1] - 1 are request b's newest tokens: with n of them, they take the context's positions
+ * seq_len[b] - n .. seq_len[b] - 1, position m being row m % 64 of page page_table[b][m / 64].  For each
+ * row the key's and the query heads' pairs are rotated, in fp32,
+ *   (x_j, x_{j+64}) -> (x_j c - x_{j+64} s, x_{j+64} c + x_j s)
+ * by the cos c and sin s of its position; the queries are rounded to bf16 into q_out, the keys (rounded
+ * to bf16, or from fp32 to the 4-bit format) and the values go to the cache, page_cnt is raised and
+ * the sub-block sums that changed are formed again in paged_kv_append's order.
+ *   k_new, v_new : device bf16, rows k_stride (v_stride) elements apart, each [n_kv_heads][128]
+ *   q            : device bf16, rows q_stride apart, each [Hq][128], or NULL (no queries)
+ *   q_out        : device bf16 [n_rows][Hq][128]; may be q itself where q is contiguous
+ *   row_first    : device int32 [B + 1], ascending, row_first[B] <= n_rows; NULL: row b is request b's
+ *                  (n_rows == B).  Rows that it gives to no request (padding) are left alone, in q_out too.
+ *   seq_len      : device int32 [B], tokens of the context with the new ones
+ *   rope         : NULL appends k_new as it is (q must then be NULL)
+ * Pointers 16-byte aligned; strides multiples of 8, at least a row.  No two requests may share a page that
+ * is written (as decode_append_score).  A row whose page is outside the table or the pool is not appended
+ * (SPKV_DEVERR_PAGE_ID / _PHYS); one with a position outside [0, n_pos) is neither appended nor has it
+ * queries out (SPKV_DEVERR_POS), and its sub-block's sums are formed without it.  The handle must have
+ * summaries and be of the current device (else SPKV_EINVAL). */
+int paged_kv_append_rope(spkv_cache_t cache, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         int n_rows, int B, const int32_t* row_first, const int32_t* seq_len,
+                         const int32_t* page_table, int np_max, const spkv_rope* rope, const void* q, int64_t q_stride,
+                         int Hq, void* q_out, void* stream);
+
+/* Pages of a 4-bit cache as bf16 pages, for the calls that read bf16 pools (a prefill over cached pages,
+ * column scores): listed page i of head h goes to k_out[h][i], v_out[h][i], each value code s g rounded
+ * once to bf16.
+ *   pages        : device int32 [n_pages], physical pages (one outside the pool is skipped: SPKV_DEVERR_PHYS)
+ *   k_out, v_out : device bf16 [n_kv_heads][n_pages][64][128], 16-byte aligned; rows at and behind
+ *                  page_cnt of a page are left as they are (a handle without page_cnt: all 64 are written)
+ * SPKV_EUNSUPPORTED for a bf16 handle, SPKV_EINVAL for another device's. */
+int paged_kv_unpack_q4(spkv_cache_t cache, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream);
 
 /* Block scores, [NOSA] "Method 1", block-wise implementation (two-stage pooling: mean over
  * each 16-token sub-block, max over the 4 sub-blocks of the page) and dual selection
@@ -557,7 +649,7 @@ int spkv_pagemap_bytes(spkv_pagemap_t pm, int64_t* device_bytes, int64_t* host_b
 /* Frees everything the manager allocated (the caller ensures no kernel still reads it). */
 int spkv_pagemap_destroy(spkv_pagemap_t pm);
 
-/* Waits for `stream`, then reads and clears the handle's device error word into *bits./* Waits for `stream`, then reads and clears the handle's device error word into *bits.
+/* Waits for `stream`, then reads and clears the handle's device error word into *bits.
  * Returns SPKV_OK when it was zero, SPKV_EDEVICE otherwise (SPKV_ECUDA if the wait failed). */
 int spkv_get_device_error(spkv_cache_t cache, void* stream, uint32_t* bits);
 

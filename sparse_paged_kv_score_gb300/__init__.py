@@ -19,6 +19,14 @@ With the full pool offloaded to pinned host memory and a slot pool on the device
     slots = paged_kv_create(k_slots, v_slots, None, None)
     retrieve_pages(slots, k_host, v_host, page_table, missing, n_missing, victims, slot, n_sel, n_slots)
     sparse_decode_attn_slots(slots, q, sel, slot, n_sel, n_slots, seq_len, out, lse)
+
+With the cache held in 4 bits, and the rotary positions applied where rows are appended:
+
+    cache = paged_kv_create_q4(kv_pool, k_scale, v_scale, ksum, page_cnt)
+    paged_kv_append_rope(cache, k, v, seq_len, page_table, q=q, q_out=q_rot, cos_sin=cos_sin)
+    score_blocks(cache, q_rot, page_table, seq_len, scores)   # and select_topk, as above
+    sparse_decode_attn(cache, q_rot, page_table, sel, n_sel, seq_len, out, lse)
+    paged_kv_unpack_q4(cache, pages, k_pages, v_pages)        # bf16 pages for a prefill
 """
 from __future__ import annotations
 
@@ -27,7 +35,7 @@ import ctypes
 import numpy as np
 import torch
 
-from ._abi import DEVERR, SpkvDesc, SpkvError, SpkvPageDir, check, load
+from ._abi import DEVERR, SpkvDesc, SpkvDescQ4, SpkvError, SpkvPageDir, SpkvRope, check, load
 
 __all__ = ["PagedKVCache", "paged_kv_create", "paged_kv_append", "score_blocks", "decode_append_score",
            "select_topk",
@@ -37,10 +45,12 @@ __all__ = ["PagedKVCache", "paged_kv_create", "paged_kv_append", "score_blocks",
            "attn_column_scores", "attn_column_scores_lse", "lazy_alibi_prefill_attn",
            "sparse_decode_attn_noalloc", "pack_page_words", "get_device_error", "SpkvError", "DEVERR",
            "PageMap", "score_blocks_dir", "sparse_decode_attn_dir", "retrieve_pages_dir", "DocPlan",
-           "lazy_rope_decode_attn_docs",
+           "lazy_rope_decode_attn_docs", "PagedKVCacheQ4", "paged_kv_create_q4", "paged_kv_append_rope",
+           "paged_kv_unpack_q4",
            "load"]
 
 HEAD_DIM, PAGE, SUBBLOCK = 128, 64, 16
+Q4_PAGE_BYTES = 9216   # one page of one kv head of a 4-bit cache
 
 
 def _stream(stream) -> int:
@@ -129,6 +139,118 @@ class PagedKVCache:
 
 def paged_kv_create(k_pool, v_pool, ksum, page_cnt, max_units: int = 0, stream=None) -> PagedKVCache:
     return PagedKVCache(k_pool, v_pool, ksum, page_cnt, max_units, stream)
+
+
+class PagedKVCacheQ4(PagedKVCache):
+    """A handle over a pool held in 4 bits: ``kv_pool`` uint8 [Hk][n_phys][9216] (keys and values of a
+    page-head together; spkv.h gives the layout), ``k_scale`` and ``v_scale`` fp32 [Hk], the heads'
+    factors.  ``ksum`` and ``page_cnt`` as for :class:`PagedKVCache`; ``page_cnt`` alone tells
+    ``paged_kv_unpack_q4`` how many rows a page holds."""
+
+    def __init__(self, kv_pool, k_scale, v_scale, ksum, page_cnt, max_units: int = 0, stream=None):
+        self.handle = None
+        if kv_pool.dim() != 3:
+            raise ValueError(f"kv_pool: expected [Hk][n_phys][{Q4_PAGE_BYTES}]")
+        Hk, n_phys = kv_pool.shape[0], kv_pool.shape[1]
+        if ksum is not None and page_cnt is None:
+            raise ValueError("ksum is given with page_cnt")
+        ksum_bf16 = ksum is not None and ksum.dtype == torch.bfloat16
+        self.desc = SpkvDescQ4(Hk, HEAD_DIM, PAGE, SUBBLOCK, n_phys,
+                               _t(kv_pool, torch.uint8, "kv_pool", (Hk, n_phys, Q4_PAGE_BYTES)),
+                               _t(k_scale, torch.float32, "k_scale", (Hk,)), _t(v_scale, torch.float32, "v_scale", (Hk,)),
+                               None if ksum is None else _t(ksum, torch.bfloat16 if ksum_bf16 else torch.float32, "ksum",
+                                                            (Hk, n_phys, 4, HEAD_DIM)),
+                               None if page_cnt is None else _t(page_cnt, torch.int32, "page_cnt", (n_phys,)),
+                               int(max_units), int(ksum_bf16))
+        _same_device(kv_pool.device, k_scale=k_scale, v_scale=v_scale, ksum=ksum, page_cnt=page_cnt)
+        self.n_kv_heads, self.n_phys = Hk, n_phys
+        self.tensors = (kv_pool, k_scale, v_scale, ksum, page_cnt)   # keep the buffers alive
+        h = ctypes.c_void_p()
+        with torch.cuda.device(kv_pool.device):
+            check("paged_kv_create_q4", load().paged_kv_create_q4(ctypes.byref(self.desc), _stream(stream),
+                                                                  ctypes.byref(h)))
+        self.handle = h
+
+
+def paged_kv_create_q4(kv_pool, k_scale, v_scale, ksum, page_cnt, max_units: int = 0, stream=None) -> PagedKVCacheQ4:
+    return PagedKVCacheQ4(kv_pool, k_scale, v_scale, ksum, page_cnt, max_units, stream)
+
+
+def _same_device(device, **tensors) -> None:
+    for name, x in tensors.items():
+        if x is not None and x.device != device:
+            raise ValueError(f"{name}: must be on {device}, the cache's device")
+
+
+def _rows(x: torch.Tensor, name: str, n: int, heads: int):
+    """Address and row stride of bf16 rows [n][heads][128] whose rows may lie apart (a slice of a
+    wider projection's output)."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if x.dtype != torch.bfloat16:
+        raise TypeError(f"{name}: expected {torch.bfloat16}, got {x.dtype}")
+    if not x.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor")
+    if tuple(x.shape) != (n, heads, HEAD_DIM):
+        raise ValueError(f"{name}: expected shape {(n, heads, HEAD_DIM)}, got {tuple(x.shape)}")
+    if x.stride(2) != 1 or (heads > 1 and x.stride(1) != HEAD_DIM):
+        raise ValueError(f"{name}: a row's heads must be contiguous")
+    return x.data_ptr(), x.stride(0) if n > 1 else heads * HEAD_DIM
+
+
+def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table, row_first=None, q=None, q_out=None,
+                         cos_sin=None, pos=None, pair_axis=None, stream=None):
+    """Appends rows k_new, v_new (bf16 [n_rows][Hk][128]; rows may be strided) to a bf16 or 4-bit cache, keys
+    rotated by their positions; q (bf16 [n_rows][Hq][128]) rotated into q_out.  row_first int32 [B + 1] gives
+    each request's rows (None: one row a request), seq_len counts the new tokens, cos_sin fp32 [n_pos][128] holds
+    the cosines and sines of the 64 pairs (None: no rotation).  pos int32 [n_rows] or [n_rows][n_axes] (None: the
+    positions in the context); with several axes pair_axis lists each pair's axis."""
+    n, Hk = k_new.shape[0], cache.n_kv_heads
+    B, np_max = page_table.shape
+    dev = cache.tensors[0].device
+    _same_device(dev, k_new=k_new, v_new=v_new, seq_len=seq_len, page_table=page_table, row_first=row_first, q=q,
+                 q_out=q_out, cos_sin=cos_sin, pos=pos)
+    kp, ks = _rows(k_new, "k_new", n, Hk)
+    vp, vs = _rows(v_new, "v_new", n, Hk)
+    rope, axes, qp, qs, Hq, qo = None, None, None, 0, 0, None
+    if cos_sin is not None:
+        n_axes = 1 if pos is None or pos.dim() == 1 else pos.shape[1]
+        if pair_axis is not None:
+            if len(pair_axis) != HEAD_DIM // 2 or not all(0 <= int(a) < n_axes for a in pair_axis):
+                raise ValueError(f"pair_axis: expected {HEAD_DIM // 2} axes below {n_axes}")
+            axes = (ctypes.c_uint8 * (HEAD_DIM // 2))(*(int(a) for a in pair_axis))
+        elif n_axes > 1:
+            raise ValueError("pair_axis: needed with several axes")
+        if pos is not None:
+            _t(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (n, n_axes))
+        rope = ctypes.byref(SpkvRope(_t(cos_sin, torch.float32, "cos_sin", (cos_sin.shape[0], HEAD_DIM)),
+                                     cos_sin.shape[0], n_axes, axes, None if pos is None else pos.data_ptr()))
+    elif pos is not None or pair_axis is not None or q is not None:
+        raise ValueError("pos, pair_axis and q are given with cos_sin")
+    if q is not None:
+        Hq = q.shape[1]
+        qp, qs = _rows(q, "q", n, Hq)
+        if q_out is None:
+            raise ValueError("q_out: needed with q")
+        qo = _t(q_out, torch.bfloat16, "q_out", (n, Hq, HEAD_DIM))
+    with torch.cuda.device(dev):
+        check("paged_kv_append_rope", load().paged_kv_append_rope(
+            cache.handle, kp, ks, vp, vs, n, B, None if row_first is None else _t(row_first, torch.int32, "row_first", (B + 1,)),
+            _t(seq_len, torch.int32, "seq_len", (B,)), _t(page_table, torch.int32, "page_table", (B, np_max)), np_max,
+            rope, qp, qs, Hq, qo, _stream(stream)))
+
+
+def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
+    """The listed physical pages (int32 [n]) of a 4-bit cache as bf16 pages k_out, v_out [Hk][n][64][128]
+    (rows at and behind a page's count are left as they are)."""
+    n = pages.shape[0]
+    shp = (cache.n_kv_heads, n, PAGE, HEAD_DIM)
+    dev = cache.tensors[0].device
+    _same_device(dev, pages=pages, k_out=k_out, v_out=v_out)
+    with torch.cuda.device(dev):
+        check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(
+            cache.handle, _t(pages, torch.int32, "pages", (n,)), n, _t(k_out, torch.bfloat16, "k_out", shp),
+            _t(v_out, torch.bfloat16, "v_out", shp), _stream(stream)))
 
 
 def paged_kv_append(cache: PagedKVCache, phys_page, tok_in_page, k_new, v_new, stream=None):

@@ -13,7 +13,7 @@ SO_PATH = os.path.join(_HERE, "libspkv.so")
 
 SPKV_OK, SPKV_EINVAL, SPKV_ENOMEM, SPKV_ECUDA, SPKV_EDEVICE, SPKV_ETIMEOUT, SPKV_EUNSUPPORTED = \
     0, -1, -2, -3, -4, -5, -6
-DEVERR = {"PAGE_ID": 1, "PHYS": 2, "SLOT": 4, "ORDER": 8, "CAPACITY": 16, "TIMEOUT": 32}
+DEVERR = {"PAGE_ID": 1, "PHYS": 2, "SLOT": 4, "ORDER": 8, "CAPACITY": 16, "TIMEOUT": 32, "POS": 64}
 
 # Every entry point declared in include/spkv.h, with its ctypes signature.
 _vp, _i32, _i64, _u32, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
@@ -32,11 +32,27 @@ class SpkvPageDir(ctypes.Structure):
                 ("n_host_segs", ctypes.c_int64)]
 
 
+class SpkvDescQ4(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("subblock", ctypes.c_int32),
+                ("n_phys_pages", ctypes.c_int64), ("kv_pool", _vp), ("k_scale", _vp), ("v_scale", _vp),
+                ("ksum", _vp), ("page_cnt", _vp), ("max_units", ctypes.c_int32), ("ksum_bf16", ctypes.c_int32)]
+
+
+class SpkvRope(ctypes.Structure):
+    _fields_ = [("cos_sin", _vp), ("n_pos", ctypes.c_int64), ("n_axes", ctypes.c_int32),
+                ("pair_axis", ctypes.POINTER(ctypes.c_uint8)), ("pos", _vp)]
+
+
 _pd = ctypes.POINTER(SpkvPageDir)
 
 SIGNATURES = {
     "paged_kv_create": ([ctypes.POINTER(SpkvDesc), _vp, ctypes.POINTER(_vp)], _i32),
     "paged_kv_append": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp], _i32),
+    "paged_kv_create_q4": ([ctypes.POINTER(SpkvDescQ4), _vp, ctypes.POINTER(_vp)], _i32),
+    "paged_kv_append_rope": ([_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i32, ctypes.POINTER(SpkvRope), _vp,
+                              _i64, _i32, _vp, _vp], _i32),
+    "paged_kv_unpack_q4": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
     "score_blocks": ([_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
     "decode_append_score": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
     "select_topk": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp], _i32),

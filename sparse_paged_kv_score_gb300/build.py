@@ -14,7 +14,8 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libspkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
-SOURCES = ["api.cu", "attn.cu", "score.cu", "select.cu", "summary.cu", "resid.cu", "fused.cu", "prefill.cu", "colscore.cu", "retrieve.cu", "noalloc.cu", "pagemap.cu", "docplan.cu"]
+SOURCES = ["api.cu", "attn.cu", "score.cu", "select.cu", "summary.cu", "resid.cu", "fused.cu", "prefill.cu", "colscore.cu", "retrieve.cu", "noalloc.cu", "pagemap.cu", "docplan.cu",
+           "q4.cu", "append_rope.cu", "attn_q4.cu"]
 
 
 def _nvcc() -> str:

@@ -22,6 +22,12 @@ cudaStream_t as_stream(void* s) { return static_cast<cudaStream_t>(s); }
 
 int status_of(cudaError_t e) { return e == cudaSuccess ? SPKV_OK : SPKV_ECUDA; }
 
+// Whether the handle's device is the current one (its memory and its stream's kernels live there).
+bool on_device(spkv_cache_t c) {
+  int dev = -1;
+  return cudaGetDevice(&dev) == cudaSuccess && dev == c->device;
+}
+
 bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 PFN_cuTensorMapEncodeTiled_v12000 get_encode_fn() {
@@ -96,6 +102,12 @@ void fill_common(AttnParams& p, spkv_cache_t c, const void* q, int B, int Hq, fl
   p.wait_ns = c->wait_ns;
 }
 
+// The selected-pages attention in the handle's format; grid bounds the persistent bf16 kernel's CTAs.
+int launch_sparse(spkv_cache_t c, const AttnParams& p, int grid, void* stream) {
+  if (c->pool4) return on_device(c) ? status_of(spkv::launch_attn_q4(c, p, as_stream(stream))) : SPKV_EINVAL;
+  return status_of(spkv::launch_attn(c, p, false, grid, as_stream(stream)));
+}
+
 }  // namespace
 
 namespace spkv {
@@ -106,6 +118,7 @@ cudaError_t init_kernel_attributes() {
   if ((e = fused_init_attributes()) != cudaSuccess) return e;
   if ((e = prefill_init_attributes()) != cudaSuccess) return e;
   if ((e = colscore_init_attributes()) != cudaSuccess) return e;
+  if ((e = attn_q4_init_attributes()) != cudaSuccess) return e;
   return resid_init_attributes();
 }
 }  // namespace spkv
@@ -125,21 +138,28 @@ const char* spkv_status_string(int s) {
   }
 }
 
-int paged_kv_create(const spkv_desc* desc, void* stream, spkv_cache_t* out) {
-  if (!desc || !out) return SPKV_EINVAL;
-  *out = nullptr;
-  const spkv_desc& d = *desc;
+// What both cache formats check of a description besides its pools.
+static int check_desc(const spkv_desc& d) {
   if (d.head_dim != 128 || d.page_tokens != 64 || d.subblock != 16) return SPKV_EUNSUPPORTED;
   if (d.n_kv_heads <= 0 || d.n_phys_pages <= 0 || d.max_units < 0 || d.max_units > 4096) return SPKV_EINVAL;
-  if (!d.k_pool || !d.v_pool || !d.ksum != !d.page_cnt) return SPKV_EINVAL;
+  if (d.ksum && !d.page_cnt) return SPKV_EINVAL;
   if (d.ksum_bf16 != 0 && d.ksum_bf16 != 1) return SPKV_EINVAL;
-  if (!aligned(d.k_pool, 16) || !aligned(d.v_pool, 16) || !aligned(d.ksum, 16)) return SPKV_EINVAL;
+  if (!aligned(d.ksum, 16)) return SPKV_EINVAL;
+  return SPKV_OK;
+}
+
+// Allocates and initialises the handle of a checked description (4-bit: pool4 and the head scales).
+static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scale, const float* v_scale, void* stream,
+                         spkv_cache_t* out) {
   const int64_t n_ph = int64_t(d.n_kv_heads) * d.n_phys_pages;
   if (n_ph >= (int64_t(1) << 31)) return SPKV_EUNSUPPORTED;
 
   spkv_cache* c = new (std::nothrow) spkv_cache();
   if (!c) return SPKV_ENOMEM;
   c->d = d;
+  c->pool4 = pool4;
+  c->k_scale = k_scale;
+  c->v_scale = v_scale;
   c->max_units = d.max_units > 0 ? d.max_units : kMaxUnitsDefault;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess) {
@@ -151,7 +171,7 @@ int paged_kv_create(const spkv_desc* desc, void* stream, spkv_cache_t* out) {
     delete c;
     return SPKV_ECUDA;
   }
-  if (!encode_pool(&c->tmap_k, d.k_pool, n_ph) || !encode_pool(&c->tmap_v, d.v_pool, n_ph)) {
+  if (!pool4 && (!encode_pool(&c->tmap_k, d.k_pool, n_ph) || !encode_pool(&c->tmap_v, d.v_pool, n_ph))) {
     delete c;
     return SPKV_ECUDA;
   }
@@ -170,12 +190,41 @@ int paged_kv_create(const spkv_desc* desc, void* stream, spkv_cache_t* out) {
   cudaStream_t st = as_stream(stream);
   if (cudaMemsetAsync(c->dev_err, 0, sizeof(uint32_t), st) != cudaSuccess ||
       cudaMemsetAsync(c->ws_cnt, 0, sizeof(int32_t) * (2 * c->max_units + 2), st) != cudaSuccess ||
-      (d.ksum && spkv::launch_summary_build(c, st) != cudaSuccess)) {
+      (d.ksum && (pool4 ? spkv::launch_summary_build_q4(c, st) : spkv::launch_summary_build(c, st)) != cudaSuccess)) {
     paged_kv_destroy(c);
     return SPKV_ECUDA;
   }
   *out = c;
   return SPKV_OK;
+}
+
+int paged_kv_create(const spkv_desc* desc, void* stream, spkv_cache_t* out) {
+  if (!desc || !out) return SPKV_EINVAL;
+  *out = nullptr;
+  const int st = check_desc(*desc);
+  if (st != SPKV_OK) return st;
+  if (!desc->ksum != !desc->page_cnt) return SPKV_EINVAL;
+  if (!desc->k_pool || !desc->v_pool || !aligned(desc->k_pool, 16) || !aligned(desc->v_pool, 16)) return SPKV_EINVAL;
+  return create_handle(*desc, nullptr, nullptr, nullptr, stream, out);
+}
+
+int paged_kv_create_q4(const spkv_desc_q4* desc, void* stream, spkv_cache_t* out) {
+  if (!desc || !out) return SPKV_EINVAL;
+  *out = nullptr;
+  spkv_desc d = {};
+  d.n_kv_heads = desc->n_kv_heads;
+  d.head_dim = desc->head_dim;
+  d.page_tokens = desc->page_tokens;
+  d.subblock = desc->subblock;
+  d.n_phys_pages = desc->n_phys_pages;
+  d.ksum = desc->ksum;
+  d.page_cnt = desc->page_cnt;
+  d.max_units = desc->max_units;
+  d.ksum_bf16 = desc->ksum_bf16;
+  const int st = check_desc(d);
+  if (st != SPKV_OK) return st;
+  if (!desc->kv_pool || !aligned(desc->kv_pool, 16) || !desc->k_scale || !desc->v_scale) return SPKV_EINVAL;
+  return create_handle(d, static_cast<uint8_t*>(desc->kv_pool), desc->k_scale, desc->v_scale, stream, out);
 }
 
 int paged_kv_destroy(spkv_cache_t c) {
@@ -200,9 +249,78 @@ int spkv_set_wait_limit(spkv_cache_t c, uint64_t ns) {
 int paged_kv_append(spkv_cache_t c, const int32_t* phys_page, const int32_t* tok_in_page, const void* k_new,
                     const void* v_new, int n_rows, void* stream) {
   if (!c || !c->d.ksum || n_rows < 0) return SPKV_EINVAL;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (n_rows == 0) return SPKV_OK;
   if (!phys_page || !tok_in_page || !k_new || !v_new || !aligned(k_new, 4) || !aligned(v_new, 4)) return SPKV_EINVAL;
   return status_of(spkv::launch_append(c, phys_page, tok_in_page, k_new, v_new, n_rows, as_stream(stream)));
+}
+
+int paged_kv_append_rope(spkv_cache_t c, const void* k_new, int64_t k_stride, const void* v_new, int64_t v_stride,
+                         int n_rows, int B, const int32_t* row_first, const int32_t* seq_len, const int32_t* page_table,
+                         int np_max, const spkv_rope* rope, const void* q, int64_t q_stride, int Hq, void* q_out,
+                         void* stream) {
+  if (!c || !c->d.ksum || n_rows < 0 || B < 0) return SPKV_EINVAL;
+  const int Hk = c->d.n_kv_heads;
+  if (Hk > 65535) return SPKV_EUNSUPPORTED;
+  if (!row_first && n_rows != B) return SPKV_EINVAL;
+  spkv::AppendRopeParams p;
+  std::memset(&p, 0, sizeof(p));
+  if (q) {
+    if (!rope || !q_out || Hq <= 0 || Hq % Hk != 0) return SPKV_EINVAL;
+    p.G = Hq / Hk;
+    if (p.G > kMaxGroup) return SPKV_EUNSUPPORTED;
+    if (!aligned(q, 16) || !aligned(q_out, 16) || q_stride % 8 != 0 || q_stride < int64_t(Hq) * 128) return SPKV_EINVAL;
+  }
+  if (rope) {
+    if (rope->n_axes < 1 || rope->n_axes > 4 || !rope->cos_sin || !aligned(rope->cos_sin, 16) || rope->n_pos <= 0 ||
+        rope->n_pos >= (int64_t(1) << 31) || (rope->n_axes > 1 && (!rope->pos || !rope->pair_axis)))
+      return SPKV_EINVAL;
+    p.n_axes = rope->n_axes;
+    for (int j = 0; rope->n_axes > 1 && j < 64; ++j) {
+      if (rope->pair_axis[j] >= rope->n_axes) return SPKV_EINVAL;
+      p.pair_axis[j >> 5] |= static_cast<uint64_t>(rope->pair_axis[j]) << (2 * (j & 31));
+    }
+    p.pos = rope->pos;
+    p.cos_sin = rope->cos_sin;
+    p.n_pos = rope->n_pos;
+  }
+  if (n_rows == 0 || B == 0) return SPKV_OK;
+  if (!k_new || !v_new || !seq_len || !page_table || np_max <= 0) return SPKV_EINVAL;
+  if (!aligned(k_new, 16) || !aligned(v_new, 16) || k_stride % 8 != 0 || v_stride % 8 != 0 ||
+      k_stride < int64_t(Hk) * 128 || v_stride < int64_t(Hk) * 128 || !on_device(c))
+    return SPKV_EINVAL;
+  p.k_new = static_cast<const uint16_t*>(k_new);
+  p.v_new = static_cast<const uint16_t*>(v_new);
+  p.k_stride = k_stride;
+  p.v_stride = v_stride;
+  p.q = static_cast<const uint16_t*>(q);
+  p.q_stride = q_stride;
+  p.q_out = static_cast<uint16_t*>(q_out);
+  p.n_rows = n_rows;
+  p.B = B;
+  p.Hq = Hq;
+  p.row_first = row_first;
+  p.seq_len = seq_len;
+  p.page_table = page_table;
+  p.np_max = np_max;
+  p.pool = c->pool4 ? c->pool4 : static_cast<uint8_t*>(c->d.k_pool);
+  p.v_pool = static_cast<uint8_t*>(c->d.v_pool);
+  p.k_scale = c->k_scale;
+  p.v_scale = c->v_scale;
+  p.ksum = c->d.ksum;
+  p.ksum_bf16 = c->d.ksum_bf16;
+  p.page_cnt = c->d.page_cnt;
+  p.n_phys = c->d.n_phys_pages;
+  p.err = c->dev_err;
+  return status_of(spkv::launch_append_rope(c, p, as_stream(stream)));
+}
+
+int paged_kv_unpack_q4(spkv_cache_t c, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream) {
+  if (!c || n_pages < 0) return SPKV_EINVAL;
+  if (!c->pool4 || c->d.n_kv_heads > 65535) return SPKV_EUNSUPPORTED;
+  if (n_pages == 0) return SPKV_OK;
+  if (!pages || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || !on_device(c)) return SPKV_EINVAL;
+  return status_of(spkv::launch_unpack_q4(c, pages, n_pages, k_out, v_out, as_stream(stream)));
 }
 
 int score_blocks(spkv_cache_t c, const void* q, int B, int Hq, const int32_t* page_table, int np_max,
@@ -219,6 +337,7 @@ int decode_append_score(spkv_cache_t c, const void* k_new, const void* v_new, co
                         const int32_t* page_table, int np_max, const int32_t* seq_len, float* scores, void* stream) {
   int st = check_group(c, B, Hq);
   if (st != SPKV_OK) return st;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (!c->d.ksum) return SPKV_EINVAL;
   if (B == 0) return SPKV_OK;
   if (!q || !page_table || !seq_len || !scores || np_max <= 0 || !aligned(q, 8)) return SPKV_EINVAL;
@@ -258,7 +377,7 @@ int sparse_decode_attn(spkv_cache_t c, const void* q, int B, int Hq, const int32
   p.min_chunk = (sel_stride + 125) / 126;
   const int64_t t_max = int64_t(B) * c->d.n_kv_heads * sel_stride;
   const int grid = static_cast<int>(t_max < c->attn_grid ? t_max : c->attn_grid);
-  return status_of(spkv::launch_attn(c, p, false, grid, as_stream(stream)));
+  return launch_sparse(c, p, grid, stream);
 }
 
 int sparse_decode_attn_slots(spkv_cache_t c, const void* q, int B, int Hq, const int32_t* sel, const int32_t* slot,
@@ -283,7 +402,7 @@ int sparse_decode_attn_slots(spkv_cache_t c, const void* q, int B, int Hq, const
   p.min_chunk = (sel_stride + 125) / 126;
   const int64_t t_max = int64_t(B) * c->d.n_kv_heads * sel_stride;
   const int grid = static_cast<int>(t_max < c->attn_grid ? t_max : c->attn_grid);
-  return status_of(spkv::launch_attn(c, p, false, grid, as_stream(stream)));
+  return launch_sparse(c, p, grid, stream);
 }
 
 int lazy_rope_decode_attn(spkv_cache_t c, const void* q, int B, int Hq, const int32_t* qpos, const uint32_t* meta,
@@ -291,6 +410,7 @@ int lazy_rope_decode_attn(spkv_cache_t c, const void* q, int B, int Hq, const in
                           float theta, float* out, float* lse, void* stream) {
   int st = check_group(c, B, Hq);
   if (st != SPKV_OK) return st;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (B == 0) return SPKV_OK;
   if (!q || !qpos || !meta || !n_pages || !doc_pos || !out || !lse || np_max <= 0 || max_docs <= 0 ||
       !aligned(q, 16))
@@ -322,6 +442,7 @@ static int rope_prefill(spkv_cache_t c, const void* q, int B, int T, int Hq, con
                         const int32_t* page_start, const int32_t* doc_pos, int max_docs, float theta, float* out,
                         float* lse, void* stream) {
   if (!c || B < 0 || T < 0 || Hq <= 0) return SPKV_EINVAL;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   if (Hq / Hk > kMaxGroup) return SPKV_EUNSUPPORTED;
@@ -382,6 +503,7 @@ int lazy_alibi_prefill_attn(spkv_cache_t c, const void* q, int B, int T, int Hq,
                             const int32_t* page_start, const int32_t* doc_pos, int max_docs, const float* slopes,
                             float* out, float* lse, void* stream) {
   if (!c || B < 0 || T < 0 || Hq <= 0) return SPKV_EINVAL;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   if (Hq / Hk > kMaxGroup) return SPKV_EUNSUPPORTED;
@@ -419,6 +541,7 @@ int lazy_alibi_prefill_attn(spkv_cache_t c, const void* q, int B, int T, int Hq,
 static int column_scores(spkv_cache_t c, const void* q, const float* lse_in, int B, int alpha, int Hq,
                   const int32_t* page_table, int np_max, const int32_t* seq_len, float* scores, void* stream) {
   if (!c || B < 0 || Hq <= 0 || alpha < 0) return SPKV_EINVAL;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   if (alpha > kMaxColumnRows || Hq / Hk > kMaxGroup) return SPKV_EUNSUPPORTED;
@@ -530,6 +653,7 @@ static int retrieve_common(spkv_cache_t c, const void* k_host, const void* v_hos
                            const int32_t* missing, const int32_t* n_missing, const int32_t* victims, int32_t* slot,
                            const int32_t* n_sel, int sel_stride, int n_slots, void* stream) {
   if (!c || B < 0) return SPKV_EINVAL;
+  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (B == 0) return SPKV_OK;
   if (!k_host || !v_host || (!page_table && !pd) || !missing || !n_missing || !victims || !slot || !n_sel)
     return SPKV_EINVAL;
@@ -646,7 +770,7 @@ int sparse_decode_attn_dir(spkv_cache_t c, const void* q, int B, int Hq, const s
   p.min_chunk = (sel_stride + 125) / 126;
   const int64_t t_max = int64_t(B) * c->d.n_kv_heads * sel_stride;
   const int grid = static_cast<int>(t_max < c->attn_grid ? t_max : c->attn_grid);
-  return status_of(spkv::launch_attn(c, p, false, grid, as_stream(stream)));
+  return launch_sparse(c, p, grid, stream);
 }
 
 int retrieve_pages_dir(spkv_cache_t c, const void* k_host, const void* v_host, int64_t n_host_pages,

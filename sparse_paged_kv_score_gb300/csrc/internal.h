@@ -29,6 +29,9 @@ struct spkv_cache {
   const void* host_v = nullptr;
   const void* host_k_dev = nullptr;
   const void* host_v_dev = nullptr;
+  uint8_t* pool4 = nullptr;      // 4-bit handle: its pool [Hk][n_phys][9216] (no tensor maps, d.k_pool unused)
+  const float* k_scale = nullptr;   // 4-bit handle: [Hk]
+  const float* v_scale = nullptr;
 };
 
 namespace spkv {
@@ -157,7 +160,50 @@ struct ColScoreParams {
   uint32_t* err;
 };
 
+// Parameters of the attention over a 4-bit pool (sparse forms only: a.qpos and what follows unused).
+struct AttnQ4Params {
+  AttnParams a;
+  const uint8_t* pool;
+  const float* k_scale;
+  const float* v_scale;
+};
+
+// Parameters of the rotating append (either cache format).
+struct AppendRopeParams {
+  const uint16_t* k_new;         // bf16 rows, k_stride elements apart, [Hk][128] each
+  const uint16_t* v_new;
+  const uint16_t* q;             // null: no queries
+  int64_t k_stride, v_stride, q_stride;
+  uint16_t* q_out;               // [n_rows][Hq][128]
+  int n_rows, B, Hq, G;          // G = 0 without queries
+  const int32_t* row_first;      // [B + 1] or null: row i is request i's
+  const int32_t* seq_len;
+  const int32_t* page_table;
+  int np_max;
+  int n_axes;
+  const int32_t* pos;            // [n_rows][n_axes] or null: the position in the context
+  const float* cos_sin;          // [n_pos][128] or null: no rotation
+  int64_t n_pos;
+  uint64_t pair_axis[2];         // two bits a pair
+  int window;                    // rows per CTA (set by the launch)
+  uint8_t* pool;                 // key pool (bf16) or the 4-bit pool
+  uint8_t* v_pool;               // bf16 form
+  const float* k_scale;
+  const float* v_scale;
+  void* ksum;
+  int ksum_bf16;
+  int32_t* page_cnt;
+  int64_t n_phys;
+  uint32_t* err;
+};
+
 cudaError_t launch_summary_build(const spkv_cache* c, cudaStream_t st);
+cudaError_t launch_summary_build_q4(const spkv_cache* c, cudaStream_t st);
+cudaError_t launch_append_rope(const spkv_cache* c, AppendRopeParams& p, cudaStream_t st);
+cudaError_t launch_unpack_q4(const spkv_cache* c, const int32_t* pages, int n_pages, void* k_out, void* v_out,
+                             cudaStream_t st);
+cudaError_t launch_attn_q4(const spkv_cache* c, const AttnParams& a, cudaStream_t st);
+cudaError_t attn_q4_init_attributes();
 cudaError_t launch_append(const spkv_cache* c, const int32_t* phys, const int32_t* tok, const void* k_new,
                           const void* v_new, int n_rows, cudaStream_t st);
 // The fused decode append's pointers (k_new, v_new: bf16 [B][Hk][128] as 32-bit words).

@@ -1,0 +1,318 @@
+"""The 4-bit cache on the GPU: what it holds, the attention over it, and its pages back as bf16."""
+import numpy as np
+import pytest
+import torch
+
+import q4_ref as ref
+import sparse_paged_kv_score_gb300 as spkv
+from helpers import DEV, bf, f32, host_bits, i32
+
+pytestmark = pytest.mark.gpu
+
+
+def u8(a):
+    return torch.from_numpy(np.ascontiguousarray(a, np.uint8)).to(DEV)
+
+
+class Cache:
+    """A 4-bit cache of N(0, 1) rows with its handle; page p of request b is page_table[b, p]."""
+
+    def __init__(self, Hk, B, np_max, seq_len, seed=0, junk=False, sums=True, ksum_dtype=torch.float32, key_scale=1.0):
+        rng = np.random.default_rng(seed)
+        self.Hk, self.B, self.np_max = Hk, B, np_max
+        self.n_phys = B * np_max + 1
+        self.gk = (rng.uniform(0.5, 2, Hk) * 5 / 2688).astype(np.float32)
+        self.gv = (rng.uniform(0.5, 2, Hk) * 5 / 2688).astype(np.float32)
+        shape = (Hk, self.n_phys, 64, 128)
+        self.blob = ref.pool_of(ref.bf16(rng.standard_normal(shape) * key_scale), ref.bf16(rng.standard_normal(shape)),
+                                self.gk, self.gv)
+        self.pt = rng.permutation(self.n_phys)[:B * np_max].reshape(B, np_max).astype(np.int32)
+        self.L = np.asarray(seq_len, np.int32)
+        self.cnt = np.zeros(self.n_phys, np.int32)
+        for b in range(B):
+            for p in range((int(self.L[b]) + 63) // 64):
+                self.cnt[self.pt[b, p]] = min(64, self.L[b] - 64 * p)
+        if junk:   # bytes behind a page's last token: every scale NaN, codes all ones
+            for p in range(self.n_phys):
+                for t in range(self.cnt[p], 64):
+                    for at in (ref.KC, ref.VC, ref.KS, ref.VS):
+                        self.blob[:, p, at[t]] = 0xFF
+        self.pool = u8(self.blob)
+        self.ksum = torch.zeros(Hk, self.n_phys, 4, 128, dtype=ksum_dtype, device=DEV) if sums else None
+        self.cnt_d = i32(self.cnt) if sums else None
+        self.gk_d, self.gv_d = f32(self.gk), f32(self.gv)
+        self.handle = spkv.paged_kv_create_q4(self.pool, self.gk_d, self.gv_d, self.ksum, self.cnt_d, max_units=B * Hk)
+
+    def select(self, stride, rng, counts=None):
+        """Random ascending selections; each ends with the local page unless counts says how many."""
+        sel = np.full((self.B, self.Hk, stride), -1, np.int32)
+        n = np.zeros((self.B, self.Hk), np.int32)
+        for b in range(self.B):
+            pages = (int(self.L[b]) + 63) // 64
+            for h in range(self.Hk):
+                k = min(stride, pages) if counts is None else min(stride, pages, int(counts[b, h]))
+                x = rng.permutation(pages - 1)[:max(0, k - 1)] if pages > 1 else np.zeros(0, int)
+                lst = sorted(list(x) + [pages - 1])[:k]
+                sel[b, h, :k], n[b, h] = lst[:k], k
+        return sel, n
+
+    def attend(self, q, sel, n, **kw):
+        B, Hq = q.shape[:2]
+        out = torch.full((B, Hq, 128), 7.0, device=DEV)
+        lse = torch.full((B, Hq), 7.0, device=DEV)
+        spkv.sparse_decode_attn(self.handle, q, i32(self.pt), i32(sel), i32(n), i32(self.L), out, lse, **kw)
+        return out, lse
+
+
+def queries(B, Hq, seed=1, scale=1.0):
+    x = ref.bf16(np.random.default_rng(seed).standard_normal((B, Hq, 128)) * scale)
+    return x, bf(ref.bf16_bits(x))
+
+
+def check(out, lse, want):
+    o, l, eo, el = want
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    empty = np.isneginf(l)
+    assert np.array_equal(empty, np.isneginf(lse))
+    assert np.all(out[empty] == 0)
+    d = np.abs(out - o).max(-1)
+    assert np.all(d <= eo), (d / np.maximum(eo, 1e-30)).max()
+    d = np.abs(lse[~empty] - l[~empty])
+    assert np.all(d <= el[~empty]), (d / el[~empty]).max()
+
+
+@pytest.mark.parametrize("Hq,Hk", [(8, 2), (1, 1), (3, 3), (6, 2), (5, 1), (8, 1), (18, 2), (16, 1)])
+@pytest.mark.parametrize("L", [1, 15, 64, 65, 400])
+def test_attention_sizes(Hq, Hk, L):
+    B = 3
+    c = Cache(Hk, B, (L + 63) // 64 + 1, [L, max(1, L - 1), max(1, L // 2)], seed=L, junk=True)
+    rng = np.random.default_rng(L)
+    sel, n = c.select(max(1, (L + 63) // 64), rng)
+    qx, q = queries(B, Hq)
+    out, lse = c.attend(q, sel, n)
+    assert spkv.get_device_error(c.handle) == (0, 0)
+    check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
+
+
+@pytest.mark.parametrize("Hq,Hk", [(8, 2), (10, 2), (16, 1)])
+def test_attention_ragged_selections(Hq, Hk):
+    """Selections of every length, empty ones too, many pages in one of them."""
+    B = 9
+    c = Cache(Hk, B, 70, [4480, 1, 64, 100, 900, 4000, 65, 2222, 4410], seed=5, junk=True)
+    rng = np.random.default_rng(2)
+    counts = rng.integers(0, 68, (B, Hk))
+    counts[0], counts[1], counts[4] = 67, 0, 0
+    sel, n = c.select(67, rng, counts)
+    qx, q = queries(B, Hq)
+    out, lse = c.attend(q, sel, n)
+    assert spkv.get_device_error(c.handle) == (0, 0)
+    check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
+
+
+@pytest.mark.parametrize("q_scale,key_scale", [(1e-6, 1.0), (30.0, 1.0), (1e4, 1e-3), (1.0, 0.0)])
+def test_attention_score_ranges(q_scale, key_scale):
+    """Flat and peaked weights, queries outside f16's range, keys of zeros: the running maximum rises."""
+    c = Cache(2, 2, 9, [530, 77], seed=7, key_scale=key_scale)
+    sel, n = c.select(9, np.random.default_rng(3))
+    qx, q = queries(2, 8, scale=q_scale)
+    out, lse = c.attend(q, sel, n)
+    check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
+
+
+def test_attention_rising_scores():
+    """Each page's keys score far above the last one's, so the reference moves at every page."""
+    c = Cache(1, 1, 12, [12 * 64 - 5], seed=8)
+    k = np.zeros((1, c.n_phys, 64, 128), np.float32)
+    qx, q = queries(1, 4, seed=9)
+    for p in range(12):
+        k[0, c.pt[0, p]] = ref.bf16(qx[0, 0] * (0.02 * (p + 1) ** 2))
+    v = ref.bf16(np.random.default_rng(4).standard_normal(k.shape))
+    c.blob[:] = ref.pool_of(k, v, c.gk, c.gv)
+    c.pool.copy_(u8(c.blob))
+    sel, n = c.select(12, np.random.default_rng(3))
+    out, lse = c.attend(q, sel, n)
+    check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
+
+
+def test_attention_passes_nan_on():
+    """A NaN key scale of an attended token makes its unit's outputs NaN, and no other unit's."""
+    c = Cache(2, 2, 3, [150, 150], seed=11)
+    c.blob[0, c.pt[0, 1], ref.KS[5]] = 0x7F
+    c.pool.copy_(u8(c.blob))
+    sel, n = c.select(3, np.random.default_rng(3))
+    _, q = queries(2, 8)
+    out, lse = c.attend(q, sel, n)
+    assert torch.isnan(out[0, :4]).all() and torch.isnan(lse[0, :4]).all()
+    assert torch.isfinite(out[0, 4:]).all() and torch.isfinite(out[1]).all()
+
+
+def test_attention_bad_entries_are_skipped():
+    """Page ids and physical pages out of range are flagged and left out; the others attend."""
+    c = Cache(2, 2, 6, [380, 200], seed=12)
+    sel, n = c.select(4, np.random.default_rng(3))
+    good, gn = sel.copy(), n.copy()
+    sel[0, 1, 1] = 6            # past the table
+    good[0, 1], gn[0, 1] = np.concatenate([np.delete(good[0, 1], 1), [-1]]), n[0, 1] - 1
+    pt = c.pt.copy()
+    dead = int(sel[1, 0, 0])
+    pt[1, dead] = c.n_phys
+    for h in range(2):
+        keep = [x for x in good[1, h, :gn[1, h]] if x != dead]
+        good[1, h, :], gn[1, h] = -1, len(keep)
+        good[1, h, :len(keep)] = keep
+    qx, q = queries(2, 8)
+    out, lse = torch.zeros(2, 8, 128, device=DEV), torch.zeros(2, 8, device=DEV)
+    spkv.sparse_decode_attn(c.handle, q, i32(pt), i32(sel), i32(n), i32(c.L), out, lse)
+    st, bits = spkv.get_device_error(c.handle)
+    assert st == -4 and bits == spkv.DEVERR["PAGE_ID"] | spkv.DEVERR["PHYS"]
+    check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, good, gn, c.L))
+
+
+def test_attention_through_slots_and_directory():
+    """The slot and page-directory forms give bit for bit what the flat table gives."""
+    B, Hk, Hq = 3, 2, 8
+    c = Cache(Hk, B, 20, [1280, 900, 70], seed=13)
+    rng = np.random.default_rng(5)
+    sel, n = c.select(7, rng)
+    _, q = queries(B, Hq)
+    out, lse = c.attend(q, sel, n)
+    pm = spkv.PageMap(B, 20, seg_shift=4, n_dev_segs=2)
+    for b in range(B):
+        pm.map(b, 0, c.pt[b])
+    pm.promote(0, 3)
+    pm.sync()
+    o2, l2 = torch.zeros_like(out), torch.zeros_like(lse)
+    spkv.sparse_decode_attn_dir(c.handle, q, pm, i32(sel), i32(n), i32(c.L), o2, l2)
+    assert torch.equal(o2, out) and torch.equal(l2, lse)
+    # a pool of slots: unit (b, h)'s i-th page in slot 6 - i
+    slots = torch.zeros(Hk, B * 8, 9216, dtype=torch.uint8, device=DEV)
+    slot = np.full_like(sel, -1)
+    for b in range(B):
+        for h in range(Hk):
+            for i in range(n[b, h]):
+                slot[b, h, i] = 6 - i
+                slots[h, b * 8 + 6 - i] = c.pool[h, int(c.pt[b, sel[b, h, i]])]
+    s = spkv.paged_kv_create_q4(slots, c.gk_d, c.gv_d, None, None, max_units=B * Hk)
+    o3, l3 = torch.zeros_like(out), torch.zeros_like(lse)
+    spkv.sparse_decode_attn_slots(s, q, i32(sel), i32(slot), i32(n), 8, i32(c.L), o3, l3)
+    assert torch.equal(o3, out) and torch.equal(l3, lse)
+    slot[1, 0, 0] = 8
+    spkv.sparse_decode_attn_slots(s, q, i32(sel), i32(slot), i32(n), 8, i32(c.L), o3, l3)
+    assert spkv.get_device_error(s)[1] == spkv.DEVERR["SLOT"]
+    pm.close()
+
+
+def test_attention_page_order_and_repeats():
+    """Any order of pages gives the same result to rounding, and the same call the same bits."""
+    c = Cache(2, 2, 40, [2560, 2000], seed=14)
+    rng = np.random.default_rng(6)
+    sel, n = c.select(30, rng)
+    qx, q = queries(2, 8)
+    a, b = c.attend(q, sel, n), c.attend(q, sel, n)
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+
+
+def test_attention_replayed_graph_and_other_stream():
+    c = Cache(2, 4, 40, [2560, 2000, 100, 5], seed=15)
+    sel, n = c.select(30, np.random.default_rng(6))
+    qx, q = queries(4, 8)
+    want = c.attend(q, sel, n)
+    pt, s, m, L = i32(c.pt), i32(sel), i32(n), i32(c.L)
+    out, lse = torch.zeros_like(want[0]), torch.zeros_like(want[1])
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        spkv.sparse_decode_attn(c.handle, q, pt, s, m, L, out, lse)
+    side.synchronize()
+    assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        spkv.sparse_decode_attn(c.handle, q, pt, s, m, L, out, lse)
+        spkv.sparse_decode_attn(c.handle, q, pt, s, m, L, out, lse)
+    for _ in range(3):
+        out.zero_()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def test_sums_at_creation():
+    """The pooled sums: valid tokens' codes times scales in order, the head's factor once."""
+    for dtype in (torch.float32, torch.bfloat16):
+        c = Cache(2, 2, 3, [130, 33], seed=16, ksum_dtype=dtype)
+        k = ref.rows(c.blob, True).astype(np.float32)
+        want = np.zeros((2, c.n_phys, 4, 128), np.float32)
+        for p in range(c.n_phys):
+            for t in range(c.cnt[p]):
+                want[:, p, t // 16] += k[:, p, t]
+        want *= c.gk[:, None, None, None]
+        got = c.ksum.float().cpu().numpy()
+        assert np.array_equal(got, want if dtype == torch.float32 else ref.bf16(want))
+
+
+@pytest.mark.parametrize("Hk,sums", [(1, True), (3, False)])
+def test_unpack(Hk, sums):
+    """Listed pages in any order, twice too; rows behind the count and bad pages stay."""
+    c = Cache(Hk, 2, 4, [250, 64], seed=17, junk=True, sums=sums)
+    if not sums:    # counts alone
+        c.handle = spkv.paged_kv_create_q4(c.pool, c.gk_d, c.gv_d, None, i32(c.cnt), max_units=8)
+    pages = np.concatenate([c.pt[0], c.pt[1, :2], c.pt[0, :1], [c.n_phys, -1, c.n_phys - 1]]).astype(np.int32)
+    k = torch.full((Hk, len(pages), 64, 128), 3.0, dtype=torch.bfloat16, device=DEV)
+    v = k.clone()
+    spkv.paged_kv_unpack_q4(c.handle, i32(pages), k, v)
+    assert spkv.get_device_error(c.handle)[1] == spkv.DEVERR["PHYS"]
+    for out, g, keys in ((k, c.gk, True), (v, c.gv, False)):
+        x = (ref.rows(c.blob, keys).astype(np.float32) * g[:, None, None, None])
+        for i, p in enumerate(pages):
+            m = c.cnt[p] if 0 <= p < c.n_phys else 0
+            got = host_bits(out[:, i])
+            assert np.array_equal(got[:, :m], ref.bf16_bits(x[:, p, :m]) if m else got[:, :0])
+            assert np.all(got[:, m:] == 0x4040)
+
+
+def test_unpack_without_counts_and_every_code():
+    """Every code with every finite scale comes back as code * scale * g rounded to bf16."""
+    rng = np.random.default_rng(18)
+    blob = rng.integers(0, 256, (1, 8, 9216), dtype=np.uint8)
+    scales = np.concatenate([np.arange(127), 128 + np.arange(127)]).astype(np.uint8)   # no NaN
+    blob[:, :, 8192:] = scales[rng.integers(0, len(scales), (1, 8, 1024))]
+    g = np.array([0.37], np.float32)
+    h = spkv.paged_kv_create_q4(u8(blob), f32(g), f32(g), None, None, max_units=1)
+    k = torch.zeros(1, 8, 64, 128, dtype=torch.bfloat16, device=DEV)
+    v = torch.zeros_like(k)
+    spkv.paged_kv_unpack_q4(h, i32(np.arange(8)), k, v)
+    for out, keys in ((k, True), (v, False)):
+        want = ref.rows(blob, keys).astype(np.float32) * g[0]
+        assert np.array_equal(out.float().cpu().numpy(), ref.bf16(want))
+
+
+def test_refused_calls():
+    """Calls for bf16 pools refuse a 4-bit handle before anything runs."""
+    c = Cache(2, 1, 2, [100], seed=19)
+    U = -6
+    rows = torch.zeros(1, 2, 128, dtype=torch.bfloat16, device=DEV)
+    _, q = queries(1, 8)
+    one = i32([0])
+    out, lse = torch.zeros(1, 8, 128, device=DEV), torch.zeros(1, 8, device=DEV)
+    word = i32([[0, 0]])
+    calls = [
+        lambda: spkv.paged_kv_append(c.handle, one, one, rows, rows),
+        lambda: spkv.decode_append_score(c.handle, rows, rows, q, i32(c.pt), i32(c.L), torch.zeros(1, 2, 2, device=DEV)),
+        lambda: spkv.lazy_rope_decode_attn(c.handle, q, one, word, one, one.view(1, 1), 1e4, out, lse),
+        lambda: spkv.lazy_rope_prefill_attn(c.handle, q[:, None], one, word, one, one.view(1, 1), 1e4, out[:, None], lse[:, None]),
+        lambda: spkv.lazy_alibi_prefill_attn(c.handle, q[:, None], one, word, one, word, one.view(1, 1),
+                                             torch.zeros(8, device=DEV), out[:, None], lse[:, None]),
+        lambda: spkv.attn_column_scores(c.handle, q[:, None], i32(c.pt), i32(c.L), torch.zeros(1, 8, 128, device=DEV)),
+        lambda: spkv.DocPlan(c.handle, 8, np.zeros((1, 1), np.int32), np.array([0, 1], np.int32)),
+    ]
+    for f in calls:
+        with pytest.raises(spkv.SpkvError) as e:
+            f()
+        assert e.value.status == U
+    bfc = spkv.paged_kv_create(torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV),
+                               torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV), None, None, max_units=1)
+    with pytest.raises(spkv.SpkvError) as e:
+        spkv.paged_kv_unpack_q4(bfc, one, torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV),
+                                torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV))
+    assert e.value.status == U
+    assert spkv.get_device_error(c.handle) == (0, 0)
