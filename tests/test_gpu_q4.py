@@ -109,6 +109,42 @@ def test_attention_ragged_selections(Hq, Hk):
     check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
 
 
+@pytest.mark.parametrize("Hq,Hk,B,pages", [(8, 2, 8, 1200), (16, 1, 9, 2000), (6, 1, 3, 7000), (32, 8, 32, 65), (40, 8, 30, 70),
+                                             (16, 1, 200, 60)])
+def test_attention_long_lists(Hq, Hk, B, pages):
+    """More pages to a CTA than its rings hold, from few physical pages that repeat (a repeated page's
+    weights count as often as it is listed); an odd number of units of uneven lengths."""
+    c = Cache(Hk, 1, 12, [768], seed=21)
+    rng = np.random.default_rng(7)
+    which = rng.integers(0, 12, (B, pages))
+    pt = c.pt[0][which].astype(np.int32)
+    n = rng.integers(pages // 2, pages + 1, (B, Hk)).astype(np.int32)
+    n[0, 0] = pages
+    sel = np.tile(np.arange(pages, dtype=np.int32), (B, Hk, 1))
+    qx, q = queries(B, Hq)
+    out, lse = torch.zeros(B, Hq, 128, device=DEV), torch.zeros(B, Hq, device=DEV)
+    L = i32(np.full(B, 64 * pages))
+    h = spkv.paged_kv_create_q4(c.pool, c.gk_d, c.gv_d, None, None, max_units=B * Hk)
+    spkv.sparse_decode_attn(h, q, i32(pt), i32(sel), i32(n), L, out, lse)
+    assert spkv.get_device_error(h) == (0, 0)
+    G = Hq // Hk
+    out, lse = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+    for b in range(B):
+        for g in range(Hq):
+            kv = g // G
+            k = ref.rows(c.blob[kv, c.pt[0]], True).reshape(-1, 128) * float(c.gk[kv])
+            v = ref.rows(c.blob[kv, c.pt[0]], False).reshape(-1, 128) * float(c.gv[kv])
+            times = np.repeat(np.bincount(which[b, :n[b, kv]], minlength=12), 64)
+            x = k @ qx[b, g].astype(np.float64) / np.sqrt(128)
+            p = times * np.exp(x - x.max())
+            want, wl = p @ v / p.sum(), x.max() + np.log(p.sum())
+            # as ref.attention, and the fp32 sums of up to 64 pages / 14 terms a lane, rounded to nearest
+            dx = 136 * 2.0 ** -23 * (np.abs(k) @ np.abs(qx[b, g].astype(np.float64))).max() / np.sqrt(128)
+            dx += 2.0 ** -19 + pages * 4 * 2.0 ** -24
+            assert np.abs(out[b, g] - want).max() <= 2 * dx * np.abs(v).max()
+            assert abs(lse[b, g] - wl) <= dx * (1 + abs(wl))
+
+
 @pytest.mark.parametrize("q_scale,key_scale", [(1e-6, 1.0), (30.0, 1.0), (1e4, 1e-3), (1.0, 0.0)])
 def test_attention_score_ranges(q_scale, key_scale):
     """Flat and peaked weights, queries outside f16's range, keys of zeros: the running maximum rises."""
