@@ -204,6 +204,23 @@ def test_attention_bad_entries_are_skipped():
     check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, good, gn, c.L))
 
 
+def test_attention_runs_of_bad_entries():
+    """Runs of bad entries longer than any ring of stages, between good ones."""
+    c = Cache(1, 2, 8, [512, 450], seed=22)
+    good = np.stack([np.arange(7), np.arange(7)])
+    sel = np.full((2, 1, 400), 9, np.int32)      # past the table
+    at = [0, 1, 150, 151, 153, 300, 399]
+    for b in range(2):
+        sel[b, 0, at] = good[b]
+    n = np.full((2, 1), 400, np.int32)
+    qx, q = queries(2, 4)
+    out, lse = c.attend(q, sel, n)
+    assert spkv.get_device_error(c.handle)[1] == spkv.DEVERR["PAGE_ID"]
+    short = np.full((2, 1, 7), 0, np.int32)
+    short[:, 0] = good
+    check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, short, np.full((2, 1), 7), c.L))
+
+
 def test_attention_through_slots_and_directory():
     """The slot and page-directory forms give bit for bit what the flat table gives."""
     B, Hk, Hq = 3, 2, 8
