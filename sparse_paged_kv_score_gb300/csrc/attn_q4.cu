@@ -362,26 +362,31 @@ __device__ __forceinline__ int page_of(const AttnParams& p, int u, int b, int i,
 }
 
 // CTA shape: four warps, of which CG (one for every eight query heads) share a page, and a ring of NS page
-// stages.  A stage's pages all go to the same warps, so a wait that tells phases by their parity is safe.
+// stages.  The barriers of the CTA's page j are number j % L of L, a multiple of the teams and of NS, so
+// that all of a barrier's phases are waited for by the same warps: a wait tells phases by their parity.
 template <int CG, bool PACK>
 struct Cfg {
-  static constexpr int W = 4, TEAMS = W / CG, NS = 8, kThreads = W * 32;
+  static constexpr int W = 4, TEAMS = W / CG, kThreads = W * 32;
+  static constexpr int NS = PACK ? 7 : 6, L = PACK ? 28 : 12;
   static constexpr int kCols = PACK ? 4 : 8 * CG;
-  static constexpr int kDesc = kThreads;   // pages looked up at a time
-  static_assert(NS % TEAMS == 0 && kDesc % NS == 0, "stages");
+  static constexpr int kDesc = kThreads;        // pages looked up at a time
+  static constexpr int kWindow = 2 * kThreads;  // units among which they are looked up
+  static constexpr int kCtasPerSm = 3;
+  static_assert(L % NS == 0 && L % TEAMS == 0, "barriers");
 };
 
 template <int CG, bool PACK>
 struct SmemQ4 {
   using C = Cfg<CG, PACK>;
-  union {
-    uint8_t stage[C::NS][kQ4Page];
-    State<C::kCols> state[C::TEAMS];   // when the pages are through
-  };
-  uint2 desc[C::kDesc];      // place in the pool, valid tokens
-  uint64_t full[C::NS];      // a stage's copy has arrived
+  uint8_t stage[C::NS][kQ4Page];
+  State<C::kCols> state[C::TEAMS];
+  uint2 desc[C::kDesc];      // place in the pool; valid tokens, unit of the window << 8
+  uint64_t full[C::L];       // a page's copy has arrived
   int copied[C::NS];         // last page copied to a stage, -1: none
   int readers[C::NS];        // warps of a team that are through with it
+  int scan[C::kThreads];     // first page of each thread's units
+  int first[C::kWindow + 1]; // first page of each unit of the window
+  int sums[C::W];
   int last;
 };
 
@@ -396,192 +401,283 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
   if (ln == 0) p.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
 }
 
-// One CTA for a part of one unit's pages, three CTAs to an SM.  All threads look up the part's pages, each
-// page-head arrives with one bulk copy, whoever is through with a stage copies its next page there, and
-// the warps' states are merged in shared memory.  Of a unit of several parts, the CTA that arrives last
-// merges the parts in order, so the result does not depend on which one that is; every CTA arrives, so
-// the counters are zero again after the call.
+// The pages of all units form one sequence of T pages, dealt evenly to N CTAs, three to an SM so that one's
+// look-ups and merges overlap the others' pages.  A CTA's segments are the units that it meets.  All
+// threads look up its pages (128 at a time), each page-head arrives with one bulk copy, whoever is through
+// with a stage copies its next page there, and at a segment's end the warps' states are merged in shared
+// memory: into the output, or into the workspace for a unit that spans CTAs (a CTA has at most two such:
+// its first and its last).  The CTA that arrives last at such a unit merges its parts in order, so the
+// result does not depend on which one that is; every CTA arrives, so the counters are zero again after
+// the call.
 template <int CG, bool PACK>
-__global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, 3) attn_q4_kernel(const __grid_constant__ AttnQ4Params p4) {
+__global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasPerSm)
+    attn_q4_kernel(const __grid_constant__ AttnQ4Params p4) {
   using C = Cfg<CG, PACK>;
-  constexpr int TEAMS = C::TEAMS, NS = C::NS;
+  constexpr int TEAMS = C::TEAMS, NS = C::NS, L = C::L;
   extern __shared__ __align__(128) uint8_t smem_raw[];
   SmemQ4<CG, PACK>& S = *reinterpret_cast<SmemQ4<CG, PACK>*>(smem_raw);
   const AttnParams& p = p4.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int parts = p4.parts, u = blockIdx.x / parts, part = blockIdx.x % parts;
-  const int b = u / p.Hk, h = u % p.Hk;
-  const int64_t row = int64_t(b) * p.Hq + h * p.G;   // the unit's first query head
-  const int32_t* const sel = p.sel + int64_t(u) * p.sel_stride;
-  if (tid < NS) {
+  const int team = warp / CG, c8 = 8 * (warp % CG);
+  const int U = p.B * p.Hk, cta = blockIdx.x;
+  if (tid < L) {
     mbar_init(&S.full[tid], 1);
-    S.copied[tid] = -1;
-    S.readers[tid] = 0;
     fence_mbar_init();
   }
-  // What the look-ups below will want, towards L2 while the kernel before this one ends (a prefetch
-  // reads nothing).
-  if (tid == 0) {
-    prefetch_l2(p.n_sel + u);
-    prefetch_l2(p.seq_len + b);
+  if (tid < NS) {
+    S.copied[tid] = -1;
+    S.readers[tid] = 0;
   }
-  if (32 * tid < p.sel_stride && part == 0) prefetch_l2(sel + 32 * tid);
-  if (p.page_table && 32 * tid < p.np_max && part == 0) prefetch_l2(p.page_table + int64_t(b) * p.np_max + 32 * tid);
-  if (tid < 2 * p.G && part == 0) prefetch_l2(static_cast<const uint8_t*>(p.q) + row * (kHeadDim * 2) + tid * 128);
+  {
+    // What the look-ups below will want, towards L2 while the kernel before this one ends (full lists
+    // assumed; a prefetch reads nothing).
+    const int64_t x = int64_t(U) * p.sel_stride * cta / gridDim.x, at = x + 32 * tid;
+    const int u = static_cast<int>(x / p.sel_stride);
+    if (cta == 0)
+      for (int i = 32 * tid; i < U; i += 32 * C::kThreads) prefetch_l2(p.n_sel + i);
+    if (tid < 4 && at < int64_t(U) * p.sel_stride) {
+      prefetch_l2(p.sel + at);
+      if (p.slot) prefetch_l2(p.slot + at);
+    }
+    if (p.page_table && 32 * tid < p.np_max && u % p.Hk == 0) prefetch_l2(p.page_table + int64_t(u / p.Hk) * p.np_max + 32 * tid);
+    if (tid < 2 * p.G)
+      prefetch_l2(static_cast<const uint8_t*>(p.q) + (int64_t(u / p.Hk) * p.Hq + (u % p.Hk) * p.G) * (kHeadDim * 2) + tid * 128);
+  }
   pdl_wait();
   pdl_trigger();
 
-  const int n = max(0, min(p.n_sel[u], p.sel_stride));
-  const int x0 = static_cast<int>(int64_t(n) * part / parts), x1 = static_cast<int>(int64_t(n) * (part + 1) / parts);
-  if (x0 == x1) {
-    if (n == 0 && part == 0) {
-      for (int i = tid; i < p.G * kHeadDim; i += C::kThreads) p.out[row * kHeadDim + i] = 0.f;
-      if (tid < p.G) p.lse[row + tid] = -CUDART_INF_F;
+  auto count = [&](int u) { return u < U ? max(0, min(p.n_sel[u], p.sel_stride)) : 0; };
+  auto row_of = [&](int u) { return int64_t(u / p.Hk) * p.Hq + (u % p.Hk) * p.G; };   // of a unit's first query head
+  // exclusive scan over the threads; `total` of all
+  auto scan = [&](int own, int& total) {
+    int x = own;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= o) x += y;
     }
-    return;
-  }
-  Warp4<PACK> w;
-  const int team = warp / CG, c8 = 8 * (warp % CG);
-  auto copy = [&](int s, int k, int x) {   // page x of the part, k of those looked up, to stage s
-    const uint2 d = S.desc[k];
-    S.copied[s] = x;
-    mbar_arrive_expect_tx(&S.full[s], d.y > 0 ? kQ4Page : 0);
-    if (d.y > 0) bulk_load(S.stage[s], p4.pool + int64_t(d.x) * kQ4Page, kQ4Page, &S.full[s]);
-  };
-  bool ok = true;
-  for (int x = x0; x < x1; x += C::kDesc) {
-    const int cnt = min(C::kDesc, x1 - x);
-    if (tid < cnt) {
-      int phys = 0;
-      const int valid = page_of(p, u, b, x + tid, phys);
-      S.desc[tid] = make_uint2(static_cast<uint32_t>(h * p.n_phys) + phys, valid);
+    if (lane == 31) S.sums[warp] = x;
+    __syncthreads();
+    total = 0;
+    int before = 0;
+#pragma unroll
+    for (int w = 0; w < C::W; ++w) {
+      before += w < warp ? S.sums[w] : 0;
+      total += S.sums[w];
     }
     __syncthreads();
-    if (tid < min(NS, cnt)) copy(tid, tid, x - x0 + tid);
-    if (x == x0) {   // while the first pages are on their way
-      w.load_q(static_cast<const uint16_t*>(p.q) + (row + c8) * kHeadDim, p.G - c8, p.scale_log2 * p4.k_scale[h], lane);
-      w.reset();
+    return before + x - own;
+  };
+  // ---- this CTA's pages [x0, x1) of T
+  const int k = (U + C::kThreads - 1) / C::kThreads;   // consecutive units of a thread
+  int T, own = 0;
+  for (int u = tid * k; u < min(U, (tid + 1) * k); ++u) own += count(u);
+  S.scan[tid] = scan(own, T);
+  __syncthreads();
+  for (int u = cta; u < U; u += gridDim.x) {   // units without pages: zeros
+    if (count(u) > 0) continue;
+    for (int i = tid; i < p.G * kHeadDim; i += C::kThreads) p.out[row_of(u) * kHeadDim + i] = 0.f;
+    if (tid < p.G) p.lse[row_of(u) + tid] = -CUDART_INF_F;
+  }
+  const int N = min(T, static_cast<int>(gridDim.x));
+  if (cta >= N) return;
+  const int share = T / N, extra = T - share * N;   // pages of a CTA, and how many CTAs take one more
+  auto cta_begin = [&](int c) { return c * share + min(c, extra); };
+  auto cta_of = [&](int x) {
+    const int big = extra * (share + 1);
+    return x < big ? x / (share + 1) : extra + (x - big) / share;
+  };
+  const int x0 = cta_begin(cta), x1 = cta_begin(cta + 1);
+  int t0 = 0;   // the last thread whose units begin at or before x0
+#pragma unroll
+  for (int o = C::kThreads / 2; o > 0; o >>= 1)
+    if (S.scan[t0 + o] <= x0) t0 += o;
+  int base_u = t0 * k, base_x = S.scan[t0];   // the window's first unit and its first page
+
+  Warp4<PACK> w;
+  int cur = -1;        // the unit that the warps' states are of
+  bool head = true;    // whether it is the CTA's first
+  bool ok = true;
+  for (int x = x0; x < x1;) {
+    // ---- the window's units, and as many pages of theirs as there are descriptors
+    {
+      int total;
+      const int a = count(base_u + 2 * tid), b = count(base_u + 2 * tid + 1);
+      const int at = base_x + scan(a + b, total);
+      S.first[2 * tid] = at;
+      S.first[2 * tid + 1] = at + a;
+      if (tid == 0) S.first[C::kWindow] = base_x + total;
     }
-    for (int k = team; k < cnt && ok; k += TEAMS) {
-      const int s = k % NS;
-      ok = __all_sync(0xffffffffu, mbar_wait(&S.full[s], ((x - x0 + k) / NS) & 1, p.wait_ns));
-      if (!ok) break;
-      w.page(smem_u32(S.stage[s]), S.desc[k].y, lane);
-      __syncwarp();
-      if (lane == 0 && k + NS < cnt) {
-        bool free = true;
-        if (CG > 1) {   // the last of the team
-          __threadfence_block();
-          free = atomicAdd(&S.readers[s], 1) % CG == CG - 1;
-          __threadfence_block();
-        }
-        if (free) copy(s, k + NS, x - x0 + k + NS);
+    __syncthreads();
+    const int end = min(x1, S.first[C::kWindow]);   // of the pages in the window
+    const int cnt = min(C::kDesc, end - x);         // none if the window's units are all empty
+    int mine = 0;                                   // unit of page x + tid: the last that starts there or before
+#pragma unroll
+    for (int o = C::kWindow / 2; o > 0; o >>= 1)
+      if (S.first[mine + o] <= x + tid) mine += o;
+    if (tid < cnt) {
+      const int u = base_u + mine;
+      int phys = 0;
+      const uint32_t valid = page_of(p, u, u / p.Hk, x + tid - S.first[mine], phys);
+      S.desc[tid] = make_uint2(static_cast<uint32_t>((u % p.Hk) * p.n_phys) + phys, valid | mine << 8);
+    }
+    __syncthreads();
+    const int j0 = x - x0;   // the CTA's page that is the first descriptor's
+    auto copy = [&](int i) {   // descriptor i's page to its stage
+      const int j = j0 + i, s = j % NS;
+      const uint2 d = S.desc[i];
+      const bool some = (d.y & 255) != 0;
+      S.copied[s] = j;
+      uint64_t* bar = &S.full[j % L];
+      mbar_arrive_expect_tx(bar, some ? kQ4Page : 0);
+      if (some) bulk_load(S.stage[s], p4.pool + int64_t(d.x) * kQ4Page, kQ4Page, bar);
+    };
+    if (tid < min(NS, cnt) && ok) copy(tid);
+    for (int kb = 0; kb < cnt;) {
+      // ---- a segment: descriptors [kb, ke)
+      const int su = S.desc[kb].y >> 8, u = base_u + su;
+      const int f = S.first[su], e = S.first[su + 1], ke = min(cnt, e - x);
+      if (u != cur) {
+        const float factor = p.scale_log2 * p4.k_scale[u % p.Hk];
+        w.load_q(static_cast<const uint16_t*>(p.q) + (row_of(u) + c8) * kHeadDim, p.G - c8, factor, lane);
+        w.reset();
+        head = cur < 0;
+        cur = u;
       }
-      __syncwarp();
+      for (int i = kb + (team + TEAMS - (j0 + kb) % TEAMS) % TEAMS; i < ke && ok; i += TEAMS) {
+        const int j = j0 + i, s = j % NS;
+        ok = __all_sync(0xffffffffu, mbar_wait(&S.full[j % L], (j / L) & 1, p.wait_ns));
+        if (!ok) break;
+        w.page(smem_u32(S.stage[s]), S.desc[i].y & 255, lane);
+        __syncwarp();
+        if (lane == 0 && i + NS < cnt) {
+          bool free = true;
+          if (CG > 1) {   // the last of the team
+            __threadfence_block();
+            free = atomicAdd(&S.readers[s], 1) % CG == CG - 1;
+            __threadfence_block();
+          }
+          if (free) copy(i + NS);
+        }
+        __syncwarp();
+      }
+      if (!ok && lane == 0) flag_error(p.err, SPKV_DEVERR_TIMEOUT);
+      kb = ke;
+      if (x + ke < min(e, x1)) break;   // it goes on with the next descriptors
+      // ---- its end: the teams' states merged, a warp taking a query head at a time
+      w.store(S.state[team], c8, lane);
+      const float gv = p4.v_scale[u % p.Hk];
+      const bool whole = f >= x0 && e <= x1;
+      const int64_t row = row_of(u);
+      __syncthreads();
+      for (int g = warp; g < p.G; g += C::W) {
+        float M = -CUDART_INF_F, sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int t = 0; t < TEAMS; ++t) M = fmaxf(M, S.state[t].m[g]);
+#pragma unroll
+        for (int t = 0; t < TEAMS; ++t) {
+          const float m = S.state[t].m[g], l = S.state[t].l[g];
+          const float4 o = *reinterpret_cast<const float4*>(&S.state[t].o[g][4 * lane]);
+          // no token: left out (a NaN sum is not)
+          const float f = m == -CUDART_INF_F && l == 0.f ? 0.f : m == M ? 1.f : exp2f(m - M);
+          sum += f * l;
+          acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
+        }
+        if (whole) {
+          write_row(p, row + g, lane, M, sum, acc, gv);
+        } else {
+          const int64_t at = (2 * int64_t(cta) + (head ? 0 : 1)) * 16 + g;
+          *reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 4 * lane) = acc;
+          if (lane == 0) {
+            p.ws_m[at] = M;
+            p.ws_l[at] = sum;
+          }
+        }
+      }
+      __syncthreads();   // the states are free again; this CTA's part is written
+      if (whole) continue;
+      // ---- a unit of several CTAs: the last to arrive merges
+      const int c0 = cta_of(f), parts = cta_of(e - 1) - c0 + 1;
+      const int late = f > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
+      if (tid == 0) {
+        int before;   // release: this CTA's part, which the barrier has ordered before; acquire: the others'
+        asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.ws_parts + u) : "memory");
+        S.last = before == parts - 1;
+        if (S.last) p.ws_parts[u] = 0;
+      }
+      __syncthreads();
+      if (S.last) {
+        for (int g = warp; g < p.G; g += C::W) {
+          float M = -CUDART_INF_F, sum = 0.f;
+          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+          constexpr int kBatch = 8;
+          for (int i0 = 0; i0 < parts; i0 += kBatch) {
+            float m[kBatch], l[kBatch];
+            float4 o[kBatch];
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+              m[q] = -CUDART_INF_F;
+              l[q] = 0.f;
+              o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (i0 + q < parts) {
+                const int c = c0 + i0 + q;   // the unit is its CTA's first, but perhaps where it begins
+                const int64_t at = (2 * int64_t(c) + (c == c0 ? late : 0)) * 16 + g;
+                m[q] = __ldcg(p.ws_m + at);
+                l[q] = __ldcg(p.ws_l + at);
+                o[q] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * kHeadDim) + lane);
+              }
+            }
+            float mb = M;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, m[q]);
+            const float f0 = M == mb ? 1.f : exp2f(M - mb);
+            sum *= f0;
+            acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
+            M = mb;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+              const float f = m[q] == M ? 1.f : exp2f(m[q] - M);   // -inf: 0, or 1 times a zero (or NaN) state
+              sum += f * l[q];
+              acc.x += f * o[q].x, acc.y += f * o[q].y, acc.z += f * o[q].z, acc.w += f * o[q].w;
+            }
+          }
+          write_row(p, row + g, lane, M, sum, acc, gv);
+        }
+      }
     }
-    if (!ok && lane == 0) flag_error(p.err, SPKV_DEVERR_TIMEOUT);
-    if (__syncthreads_or(!ok)) break;
+    if (__syncthreads_or(!ok)) ok = false;   // the descriptors and the window are free again
+    // the next window begins with the unit of the next page, or behind this one
+    x += cnt;
+    int next = C::kWindow;
+    if (x < S.first[C::kWindow]) {
+      next = 0;
+#pragma unroll
+      for (int o = C::kWindow / 2; o > 0; o >>= 1)
+        if (S.first[next + o] <= x) next += o;
+    }
+    base_x = S.first[next];
+    base_u += next;
+    __syncthreads();
   }
   // no copy is left in flight (with the full limit: copies end in microseconds)
-  if (tid < NS && S.copied[tid] >= 0) mbar_wait(&S.full[tid], (S.copied[tid] / NS) & 1);
-  __syncthreads();
-  w.store(S.state[team], c8, lane);
-  __syncthreads();
-
-  // ---- the teams' states, by all threads: a warp takes a query head at a time
-  const float gv = p4.v_scale[h];
-  const int64_t slot0 = int64_t(u) * parts;
-  const int held = min(n, parts);   // parts that have pages
-  for (int g = warp; g < p.G; g += C::W) {
-    float M = -CUDART_INF_F, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-    for (int t = 0; t < TEAMS; ++t) M = fmaxf(M, S.state[t].m[g]);
-#pragma unroll
-    for (int t = 0; t < TEAMS; ++t) {
-      const float m = S.state[t].m[g], l = S.state[t].l[g];
-      const float4 o = *reinterpret_cast<const float4*>(&S.state[t].o[g][4 * lane]);
-      // no token: left out (a NaN sum is not)
-      const float f = m == -CUDART_INF_F && l == 0.f ? 0.f : m == M ? 1.f : exp2f(m - M);
-      sum += f * l;
-      acc.x += f * o.x, acc.y += f * o.y, acc.z += f * o.z, acc.w += f * o.w;
-    }
-    if (held == 1) {
-      write_row(p, row + g, lane, M, sum, acc, gv);
-    } else {
-      const int64_t at = (slot0 + part) * 16 + g;
-      *reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 4 * lane) = acc;
-      if (lane == 0) {
-        p.ws_m[at] = M;
-        p.ws_l[at] = sum;
-      }
-    }
-  }
-  if (held == 1) return;
-
-  // ---- the unit's parts, by the CTA that arrives last
-  __syncthreads();
-  if (tid == 0) {
-    int before;   // release: this CTA's part, which the barrier has ordered before; acquire: the others'
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.ws_parts + u) : "memory");
-    S.last = before == held - 1;
-    if (S.last) p.ws_parts[u] = 0;
-  }
-  __syncthreads();
-  if (!S.last) return;
-  for (int g = warp; g < p.G; g += C::W) {
-    float M = -CUDART_INF_F, sum = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-    constexpr int kBatch = 8;
-    for (int i0 = 0; i0 < parts; i0 += kBatch) {
-      float m[kBatch], l[kBatch];
-      float4 o[kBatch];
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        m[q] = -CUDART_INF_F;
-        l[q] = 0.f;
-        o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-        const int i = i0 + q;
-        if (i < parts && int64_t(n) * i / parts < int64_t(n) * (i + 1) / parts) {
-          const int64_t at = (slot0 + i) * 16 + g;
-          m[q] = __ldcg(p.ws_m + at);
-          l[q] = __ldcg(p.ws_l + at);
-          o[q] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * kHeadDim) + lane);
-        }
-      }
-      float mb = M;
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, m[q]);
-      const float f0 = M == mb ? 1.f : exp2f(M - mb);
-      sum *= f0;
-      acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
-      M = mb;
-#pragma unroll
-      for (int q = 0; q < kBatch; ++q) {
-        const float f = m[q] == M ? 1.f : exp2f(m[q] - M);   // -inf: 0, or 1 times a zero (or NaN) state
-        sum += f * l[q];
-        acc.x += f * o[q].x, acc.y += f * o[q].y, acc.z += f * o[q].z, acc.w += f * o[q].w;
-      }
-    }
-    write_row(p, row + g, lane, M, sum, acc, gv);
-  }
+  if (tid < NS && S.copied[tid] >= 0) mbar_wait(&S.full[S.copied[tid] % L], (S.copied[tid] / L) & 1);
 }
 
-constexpr int kPartPages = 8;      // pages of a part, at least
-constexpr int kCtasPerSm = 7;      // CTAs for an SM that the parts aim at
+constexpr int kCtaPages = 8;   // pages of a CTA, at least
 
 template <int CG, bool PACK>
-cudaError_t launch_one(const spkv_cache* c, AttnQ4Params& p, cudaStream_t st) {
+cudaError_t launch_one(const spkv_cache* c, const AttnQ4Params& p, cudaStream_t st) {
   using C = Cfg<CG, PACK>;
-  const int64_t U = int64_t(p.a.B) * p.a.Hk;
-  const int64_t want = (int64_t(kCtasPerSm) * c->sm_count + U / 2) / U;
-  p.parts = static_cast<int>(max(int64_t(1), min(want, int64_t((p.a.sel_stride + kPartPages - 1) / kPartPages))));
-  return launch_pdl(attn_q4_kernel<CG, PACK>, dim3(static_cast<unsigned>(U * p.parts)), dim3(C::kThreads),
-                    sizeof(SmemQ4<CG, PACK>), st, p);
+  const int64_t pages = int64_t(p.a.B) * p.a.Hk * p.a.sel_stride;
+  const int64_t want = (pages + kCtaPages - 1) / kCtaPages;
+  return launch_pdl(attn_q4_kernel<CG, PACK>, dim3(static_cast<unsigned>(min(want, int64_t(C::kCtasPerSm) * c->sm_count))),
+                    dim3(C::kThreads), sizeof(SmemQ4<CG, PACK>), st, p);
 }
 
 template <int CG, bool PACK>
 cudaError_t set_attr() {
+  static_assert(Cfg<CG, PACK>::kCtasPerSm * (sizeof(SmemQ4<CG, PACK>) + 1024) <= 233472, "shared memory");
   return cudaFuncSetAttribute(attn_q4_kernel<CG, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                               static_cast<int>(sizeof(SmemQ4<CG, PACK>)));
 }
@@ -596,7 +692,7 @@ cudaError_t attn_q4_init_attributes() {
 }
 
 cudaError_t launch_attn_q4(const spkv_cache* c, const AttnParams& a, cudaStream_t st) {
-  AttnQ4Params p{a, c->pool4, c->k_scale, c->v_scale, 1};
+  AttnQ4Params p{a, c->pool4, c->k_scale, c->v_scale};
   if (a.G <= 4) return launch_one<1, true>(c, p, st);
   if (a.G <= 8) return launch_one<1, false>(c, p, st);
   return launch_one<2, false>(c, p, st);

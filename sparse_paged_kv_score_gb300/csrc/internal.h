@@ -166,7 +166,6 @@ struct AttnQ4Params {
   const uint8_t* pool;
   const float* k_scale;
   const float* v_scale;
-  int parts;                     // CTAs of a unit
 };
 
 // Parameters of the rotating append (either cache format).
