@@ -388,6 +388,8 @@ struct SmemQ4 {
   int first[C::kWindow + 1]; // first page of each unit of the window
   int sums[C::W];
   int last;
+  float gv;                  // of the segment's unit: its head's value factor, its first query head
+  int64_t row;
 };
 
 __device__ __forceinline__ void prefetch_l2(const void* p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
@@ -408,8 +410,9 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
 // memory: into the output, or into the workspace for a unit that spans CTAs (a CTA has at most two such:
 // its first and its last).  The CTA that arrives last at such a unit merges its parts in order, so the
 // result does not depend on which one that is; every CTA arrives, so the counters are zero again after
-// the call.
-template <int CG, bool PACK>
+// the call.  BY_UNIT (few units, short lists): CTA c takes part c % parts of unit c / parts, which spares it
+// the search for its pages.
+template <int CG, bool PACK, bool BY_UNIT>
 __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasPerSm)
     attn_q4_kernel(const __grid_constant__ AttnQ4Params p4) {
   using C = Cfg<CG, PACK>;
@@ -433,7 +436,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     // assumed; a prefetch reads nothing).
     const int64_t x = int64_t(U) * p.sel_stride * cta / gridDim.x, at = x + 32 * tid;
     const int u = static_cast<int>(x / p.sel_stride);
-    if (cta == 0)
+    if (cta == 0 || BY_UNIT)
       for (int i = 32 * tid; i < U; i += 32 * C::kThreads) prefetch_l2(p.n_sel + i);
     if (tid < 4 && at < int64_t(U) * p.sel_stride) {
       prefetch_l2(p.sel + at);
@@ -448,6 +451,10 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
 
   auto count = [&](int u) { return u < U ? max(0, min(p.n_sel[u], p.sel_stride)) : 0; };
   auto row_of = [&](int u) { return int64_t(u / p.Hk) * p.Hq + (u % p.Hk) * p.G; };   // of a unit's first query head
+  auto write_empty = [&](int u) {
+    for (int i = tid; i < p.G * kHeadDim; i += C::kThreads) p.out[row_of(u) * kHeadDim + i] = 0.f;
+    if (tid < p.G) p.lse[row_of(u) + tid] = -CUDART_INF_F;
+  };
   // exclusive scan over the threads; `total` of all
   auto scan = [&](int own, int& total) {
     int x = own;
@@ -468,78 +475,106 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     __syncthreads();
     return before + x - own;
   };
-  // ---- this CTA's pages [x0, x1) of T
-  const int k = (U + C::kThreads - 1) / C::kThreads;   // consecutive units of a thread
-  int T, own = 0;
-  for (int u = tid * k; u < min(U, (tid + 1) * k); ++u) own += count(u);
-  S.scan[tid] = scan(own, T);
-  __syncthreads();
-  for (int u = cta; u < U; u += gridDim.x) {   // units without pages: zeros
-    if (count(u) > 0) continue;
-    for (int i = tid; i < p.G * kHeadDim; i += C::kThreads) p.out[row_of(u) * kHeadDim + i] = 0.f;
-    if (tid < p.G) p.lse[row_of(u) + tid] = -CUDART_INF_F;
-  }
-  const int N = min(T, static_cast<int>(gridDim.x));
-  if (cta >= N) return;
-  const int share = T / N, extra = T - share * N;   // pages of a CTA, and how many CTAs take one more
+  // ---- this CTA's pages [x0, x1) of T; the window of units for the look-ups, and its first page
+  int x0, x1, base_u = 0, base_x = 0;
+  int share = 1, extra = 0;   // pages of a CTA, and how many CTAs take one more
   auto cta_begin = [&](int c) { return c * share + min(c, extra); };
   auto cta_of = [&](int x) {
     const int big = extra * (share + 1);
     return x < big ? x / (share + 1) : extra + (x - big) / share;
   };
-  const int x0 = cta_begin(cta), x1 = cta_begin(cta + 1);
-  int t0 = 0;   // the last thread whose units begin at or before x0
+  // first pages of the window's units
+  auto look = [&]() {
+    int total;
+    const int a = count(base_u + 2 * tid), b = count(base_u + 2 * tid + 1);
+    const int at = base_x + scan(a + b, total);
+    S.first[2 * tid] = at;
+    S.first[2 * tid + 1] = at + a;
+    if (tid == 0) S.first[C::kWindow] = base_x + total;
+    __syncthreads();
+    return base_x + total;
+  };
+  if (BY_UNIT) {
+    base_u = cta / p4.parts;
+    const int n = count(base_u), part = cta % p4.parts;
+    x0 = static_cast<int>(int64_t(n) * part / p4.parts);
+    x1 = static_cast<int>(int64_t(n) * (part + 1) / p4.parts);
+    if (part == 0 && n == 0) write_empty(base_u);
+    if (x0 == x1) return;
+    if (tid == 0) S.first[0] = 0;
+    for (int i = tid; i < C::kWindow; i += C::kThreads) S.first[i + 1] = n;
+    __syncthreads();
+  } else {
+    int T;
+    if (U <= C::kWindow) {
+      T = look();
+    } else {   // the sums of k consecutive units a thread, then the window that begins with a thread's
+      const int k = (U + C::kThreads - 1) / C::kThreads;
+      int own = 0;
+      for (int u = tid * k; u < min(U, (tid + 1) * k); ++u) own += count(u);
+      S.scan[tid] = scan(own, T);
+      __syncthreads();
+    }
+    for (int u = cta; u < U; u += gridDim.x)
+      if (count(u) == 0) write_empty(u);
+    const int N = min(T, static_cast<int>(gridDim.x));
+    if (cta >= N) return;
+    share = T / N;
+    extra = T - share * N;
+    x0 = cta_begin(cta);
+    x1 = cta_begin(cta + 1);
+    if (U > C::kWindow) {
+      int t = 0;   // the last thread whose units begin at or before x0
 #pragma unroll
-  for (int o = C::kThreads / 2; o > 0; o >>= 1)
-    if (S.scan[t0 + o] <= x0) t0 += o;
-  int base_u = t0 * k, base_x = S.scan[t0];   // the window's first unit and its first page
+      for (int o = C::kThreads / 2; o > 0; o >>= 1)
+        if (S.scan[t + o] <= x0) t += o;
+      base_u = t * ((U + C::kThreads - 1) / C::kThreads);
+      base_x = S.scan[t];
+      look();
+    }
+  }
 
   Warp4<PACK> w;
   int cur = -1;        // the unit that the warps' states are of
   bool head = true;    // whether it is the CTA's first
   bool ok = true;
   for (int x = x0; x < x1;) {
-    // ---- the window's units, and as many pages of theirs as there are descriptors
-    {
-      int total;
-      const int a = count(base_u + 2 * tid), b = count(base_u + 2 * tid + 1);
-      const int at = base_x + scan(a + b, total);
-      S.first[2 * tid] = at;
-      S.first[2 * tid + 1] = at + a;
-      if (tid == 0) S.first[C::kWindow] = base_x + total;
-    }
-    __syncthreads();
+    // ---- as many pages as there are descriptors, and as the window has
     const int end = min(x1, S.first[C::kWindow]);   // of the pages in the window
     const int cnt = min(C::kDesc, end - x);         // none if the window's units are all empty
     int mine = 0;                                   // unit of page x + tid: the last that starts there or before
 #pragma unroll
     for (int o = C::kWindow / 2; o > 0; o >>= 1)
       if (S.first[mine + o] <= x + tid) mine += o;
-    if (tid < cnt) {
-      const int u = base_u + mine;
-      int phys = 0;
-      const uint32_t valid = page_of(p, u, u / p.Hk, x + tid - S.first[mine], phys);
-      S.desc[tid] = make_uint2(static_cast<uint32_t>((u % p.Hk) * p.n_phys) + phys, valid | mine << 8);
-    }
-    __syncthreads();
     const int j0 = x - x0;   // the CTA's page that is the first descriptor's
-    auto copy = [&](int i) {   // descriptor i's page to its stage
+    auto copy = [&](int i, uint2 d) {   // descriptor i's page to its stage
       const int j = j0 + i, s = j % NS;
-      const uint2 d = S.desc[i];
       const bool some = (d.y & 255) != 0;
       S.copied[s] = j;
       uint64_t* bar = &S.full[j % L];
       mbar_arrive_expect_tx(bar, some ? kQ4Page : 0);
       if (some) bulk_load(S.stage[s], p4.pool + int64_t(d.x) * kQ4Page, kQ4Page, bar);
     };
-    if (tid < min(NS, cnt) && ok) copy(tid);
+    if (tid < cnt) {
+      const int u = base_u + mine;
+      int phys = 0;
+      const uint32_t valid = page_of(p, u, u / p.Hk, x + tid - S.first[mine], phys);
+      const uint2 d = make_uint2(static_cast<uint32_t>((u % p.Hk) * p.n_phys) + phys, valid | mine << 8);
+      if (tid < NS && ok) copy(tid, d);
+      S.desc[tid] = d;
+    }
+    __syncthreads();
     for (int kb = 0; kb < cnt;) {
       // ---- a segment: descriptors [kb, ke)
       const int su = S.desc[kb].y >> 8, u = base_u + su;
       const int f = S.first[su], e = S.first[su + 1], ke = min(cnt, e - x);
       if (u != cur) {
-        const float factor = p.scale_log2 * p4.k_scale[u % p.Hk];
-        w.load_q(static_cast<const uint16_t*>(p.q) + (row_of(u) + c8) * kHeadDim, p.G - c8, factor, lane);
+        const int64_t row = row_of(u);
+        if (tid == 0) {
+          S.row = row;
+          S.gv = p4.v_scale[u % p.Hk];
+        }
+        w.load_q(static_cast<const uint16_t*>(p.q) + (row + c8) * kHeadDim, p.G - c8, p.scale_log2 * p4.k_scale[u % p.Hk], lane);
         w.reset();
         head = cur < 0;
         cur = u;
@@ -557,7 +592,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
             free = atomicAdd(&S.readers[s], 1) % CG == CG - 1;
             __threadfence_block();
           }
-          if (free) copy(i + NS);
+          if (free) copy(i + NS, S.desc[i + NS]);
         }
         __syncwarp();
       }
@@ -566,10 +601,10 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       if (x + ke < min(e, x1)) break;   // it goes on with the next descriptors
       // ---- its end: the teams' states merged, a warp taking a query head at a time
       w.store(S.state[team], c8, lane);
-      const float gv = p4.v_scale[u % p.Hk];
       const bool whole = f >= x0 && e <= x1;
-      const int64_t row = row_of(u);
       __syncthreads();
+      const int64_t row = S.row;
+      const float gv = S.gv;
       for (int g = warp; g < p.G; g += C::W) {
         float M = -CUDART_INF_F, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -587,7 +622,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
         if (whole) {
           write_row(p, row + g, lane, M, sum, acc, gv);
         } else {
-          const int64_t at = (2 * int64_t(cta) + (head ? 0 : 1)) * 16 + g;
+          const int64_t at = (BY_UNIT ? cta : 2 * cta + (head ? 0 : 1)) * 16 + g;
           *reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 4 * lane) = acc;
           if (lane == 0) {
             p.ws_m[at] = M;
@@ -598,12 +633,14 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       __syncthreads();   // the states are free again; this CTA's part is written
       if (whole) continue;
       // ---- a unit of several CTAs: the last to arrive merges
-      const int c0 = cta_of(f), parts = cta_of(e - 1) - c0 + 1;
-      const int late = f > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
+      const int c0 = BY_UNIT ? cta - cta % p4.parts : cta_of(f);
+      const int parts = BY_UNIT ? p4.parts : cta_of(e - 1) - c0 + 1;
+      const int late = !BY_UNIT && f > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
+      const int held = BY_UNIT ? min(e, parts) : parts;         // parts with pages
       if (tid == 0) {
         int before;   // release: this CTA's part, which the barrier has ordered before; acquire: the others'
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.ws_parts + u) : "memory");
-        S.last = before == parts - 1;
+        S.last = before == held - 1;
         if (S.last) p.ws_parts[u] = 0;
       }
       __syncthreads();
@@ -620,9 +657,10 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
               m[q] = -CUDART_INF_F;
               l[q] = 0.f;
               o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-              if (i0 + q < parts) {
-                const int c = c0 + i0 + q;   // the unit is its CTA's first, but perhaps where it begins
-                const int64_t at = (2 * int64_t(c) + (c == c0 ? late : 0)) * 16 + g;
+              const int i = i0 + q;
+              if (i < parts && (!BY_UNIT || int64_t(e) * i / parts < int64_t(e) * (i + 1) / parts)) {
+                const int c = c0 + i;   // the unit is its CTA's first, but perhaps where it begins
+                const int64_t at = (BY_UNIT ? c : 2 * c + (i == 0 ? late : 0)) * 16 + g;
                 m[q] = __ldcg(p.ws_m + at);
                 l[q] = __ldcg(p.ws_l + at);
                 o[q] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * kHeadDim) + lane);
@@ -647,8 +685,9 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       }
     }
     if (__syncthreads_or(!ok)) ok = false;   // the descriptors and the window are free again
-    // the next window begins with the unit of the next page, or behind this one
     x += cnt;
+    if (x >= x1) break;
+    // the next window begins with the unit of the next page, or behind this one
     int next = C::kWindow;
     if (x < S.first[C::kWindow]) {
       next = 0;
@@ -659,27 +698,35 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     base_x = S.first[next];
     base_u += next;
     __syncthreads();
+    if (!BY_UNIT) look();   // one unit's window stays
   }
   // no copy is left in flight (with the full limit: copies end in microseconds)
   if (tid < NS && S.copied[tid] >= 0) mbar_wait(&S.full[S.copied[tid] % L], (S.copied[tid] / L) & 1);
 }
 
-constexpr int kCtaPages = 8;   // pages of a CTA, at least
+constexpr int kCtaPages = 8;    // pages of a CTA, at least
+constexpr int kPartPages = 4;   // and of one that takes a part of a unit
 
 template <int CG, bool PACK>
-cudaError_t launch_one(const spkv_cache* c, const AttnQ4Params& p, cudaStream_t st) {
+cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
   using C = Cfg<CG, PACK>;
-  const int64_t pages = int64_t(p.a.B) * p.a.Hk * p.a.sel_stride;
-  const int64_t want = (pages + kCtaPages - 1) / kCtaPages;
-  return launch_pdl(attn_q4_kernel<CG, PACK>, dim3(static_cast<unsigned>(min(want, int64_t(C::kCtasPerSm) * c->sm_count))),
-                    dim3(C::kThreads), sizeof(SmemQ4<CG, PACK>), st, p);
+  const int64_t U = int64_t(p.a.B) * p.a.Hk, slots = int64_t(C::kCtasPerSm) * c->sm_count;
+  const dim3 block(C::kThreads);
+  const size_t smem = sizeof(SmemQ4<CG, PACK>);
+  p.parts = (p.a.sel_stride + kPartPages - 1) / kPartPages;
+  if (U * p.parts <= slots)
+    return launch_pdl(attn_q4_kernel<CG, PACK, true>, dim3(static_cast<unsigned>(U * p.parts)), block, smem, st, p);
+  const int64_t want = (U * p.a.sel_stride + kCtaPages - 1) / kCtaPages;
+  return launch_pdl(attn_q4_kernel<CG, PACK, false>, dim3(static_cast<unsigned>(min(want, slots))), block, smem, st, p);
 }
 
 template <int CG, bool PACK>
 cudaError_t set_attr() {
   static_assert(Cfg<CG, PACK>::kCtasPerSm * (sizeof(SmemQ4<CG, PACK>) + 1024) <= 233472, "shared memory");
-  return cudaFuncSetAttribute(attn_q4_kernel<CG, PACK>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              static_cast<int>(sizeof(SmemQ4<CG, PACK>)));
+  const int bytes = static_cast<int>(sizeof(SmemQ4<CG, PACK>));
+  const cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<CG, PACK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(attn_q4_kernel<CG, PACK, false>,
+                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
 }
 
 }  // namespace
@@ -692,7 +739,7 @@ cudaError_t attn_q4_init_attributes() {
 }
 
 cudaError_t launch_attn_q4(const spkv_cache* c, const AttnParams& a, cudaStream_t st) {
-  AttnQ4Params p{a, c->pool4, c->k_scale, c->v_scale};
+  const AttnQ4Params p{a, c->pool4, c->k_scale, c->v_scale, 1};
   if (a.G <= 4) return launch_one<1, true>(c, p, st);
   if (a.G <= 8) return launch_one<1, false>(c, p, st);
   return launch_one<2, false>(c, p, st);

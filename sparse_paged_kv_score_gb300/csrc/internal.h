@@ -166,6 +166,7 @@ struct AttnQ4Params {
   const uint8_t* pool;
   const float* k_scale;
   const float* v_scale;
+  int parts;                     // CTAs of a unit, where each takes a part of one
 };
 
 // Parameters of the rotating append (either cache format).
