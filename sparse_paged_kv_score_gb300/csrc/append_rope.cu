@@ -77,32 +77,43 @@ __device__ __forceinline__ uint4 load_pairs(const uint16_t* row, int l) {
   return make_uint4(a.x, a.y, b.x, b.y);
 }
 
+__device__ __forceinline__ float2 pair(uint32_t w) { return make_float2(bf16lo_to_f32(w), bf16hi_to_f32(w)); }
+
+// Cosines and sines of pairs 4l .. 4l + 3.
 struct CosSin {
-  float c[4], s[4];
+  float2 c[2], s[2];
 };
-// x: those dims, rotated (with `turn`) in fp32.
+// x: a row's dims 4l .. + 3, 64 + 4l .. + 3, rotated (with `turn`) in fp32: products and sums rounded one by
+// one (packed f32x2 products and sums were contracted: 1 value in 10^5 came out otherwise).
 __device__ __forceinline__ void rotate(uint4 v, const CosSin& t, bool turn, float (&x)[8]) {
-  const float lo[4] = {bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y)};
-  const float hi[4] = {bf16lo_to_f32(v.z), bf16hi_to_f32(v.z), bf16lo_to_f32(v.w), bf16hi_to_f32(v.w)};
+  const uint32_t a[2] = {v.x, v.y}, b[2] = {v.z, v.w};
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    x[j] = turn ? __fsub_rn(__fmul_rn(lo[j], t.c[j]), __fmul_rn(hi[j], t.s[j])) : lo[j];
-    x[4 + j] = turn ? __fadd_rn(__fmul_rn(hi[j], t.c[j]), __fmul_rn(lo[j], t.s[j])) : hi[j];
+  for (int j = 0; j < 2; ++j) {
+    float2 lo = pair(a[j]), hi = pair(b[j]);
+    if (turn) {
+      const float2 y = lo, z = hi, c = t.c[j], s = t.s[j];
+      lo.x = __fsub_rn(__fmul_rn(y.x, c.x), __fmul_rn(z.x, s.x));
+      lo.y = __fsub_rn(__fmul_rn(y.y, c.y), __fmul_rn(z.y, s.y));
+      hi.x = __fadd_rn(__fmul_rn(z.x, c.x), __fmul_rn(y.x, s.x));
+      hi.y = __fadd_rn(__fmul_rn(z.y, c.y), __fmul_rn(y.y, s.y));
+    }
+    x[2 * j] = lo.x, x[2 * j + 1] = lo.y;
+    x[4 + 2 * j] = hi.x, x[5 + 2 * j] = hi.y;
   }
 }
-// Rounds x to bf16, to a row's dims 4l .. and 64 + 4l ..
-__device__ __forceinline__ uint4 store_pairs(uint16_t* row, int l, const float (&x)[8]) {
-  const uint4 v = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
-  if (row) {
-    *reinterpret_cast<uint2*>(row + 4 * l) = make_uint2(v.x, v.y);
-    *reinterpret_cast<uint2*>(row + 64 + 4 * l) = make_uint2(v.z, v.w);
-  }
-  return v;
+// x rounded to bf16, as load_pairs gives a row.
+__device__ __forceinline__ uint4 round_pairs(const float (&x)[8]) {
+  return make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+}
+__device__ __forceinline__ void store_pairs(uint16_t* row, int l, uint4 v) {
+  *reinterpret_cast<uint2*>(row + 4 * l) = make_uint2(v.x, v.y);
+  *reinterpret_cast<uint2*>(row + 64 + 4 * l) = make_uint2(v.z, v.w);
 }
 
 template <bool Q4>
 __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
   __shared__ RowInfo info[kMaxRows];
+  __shared__ int axis_pos[kMaxRows][4];
   __shared__ __align__(16) float rows[kMaxRows][kHeadDim];   // the cache's values of the new keys (4-bit: without g)
   pdl_wait();
   pdl_trigger();
@@ -111,57 +122,74 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
   const int h = blockIdx.y, base = blockIdx.x * p.window;
   const int own = min(p.window, p.n_rows - base);
   const float gk = Q4 ? p.k_scale[h] : 1.f, gv = Q4 ? p.v_scale[h] : 1.f;
+  const bool turn = p.cos_sin != nullptr;
 
-  for (int r = warp; r < p.window + kSubblock - 1; r += n_warps) {
+  // ---- the first row's key, value and query heads are on their way while the rows' places are looked up
+  uint4 kv, qv[kHeads];
+  auto ask = [&](int r) {
     const int64_t i = base + r;
-    if (r >= own && (own < p.window || i >= p.n_rows)) break;
-    // ---- the row's key, value and first query heads are on their way while its place is looked up
-    const uint4 kv = half == 0 ? load_pairs(p.k_new + i * p.k_stride + h * kHeadDim, l)
-                               : *reinterpret_cast<const uint4*>(p.v_new + i * p.v_stride + h * kHeadDim + 8 * l);
-    const uint16_t* q = p.q + i * p.q_stride + int64_t(h) * p.G * kHeadDim;
-    uint4 qv[kHeads];
+    kv = half == 0 ? load_pairs(p.k_new + i * p.k_stride + h * kHeadDim, l)
+                   : *reinterpret_cast<const uint4*>(p.v_new + i * p.v_stride + h * kHeadDim + 8 * l);
+    const uint16_t* q = p.q + i * p.q_stride + (h * p.G + half) * kHeadDim;
 #pragma unroll
     for (int k = 0; k < kHeads; ++k)
-      if (r < own && 2 * k + half < p.G) qv[k] = load_pairs(q + (2 * k + half) * kHeadDim, l);
-    int axis_pos[4] = {0, 0, 0, 0};
-    uint32_t bad = 0;
-    const RowInfo ri = find_row(p, static_cast<int>(i), axis_pos, bad);
-    if (r >= own) {   // of the sub-block of this window's last row?
-      if (ri.b < 0 || ri.at - ri.first < r - own + 1 || ri.at % kSubblock < r - own + 1) break;
-    } else if (lane == 0 && h == 0) {
-      flag_error(p.err, bad);
-    }
-    if (lane == 0) info[r] = ri;
-    CosSin t{};
-    if (p.cos_sin && ri.rot) {
-      if (p.n_axes == 1) {
-        const float* cs = p.cos_sin + int64_t(axis_pos[0]) * kHeadDim + 4 * l;
-        const float4 c = *reinterpret_cast<const float4*>(cs), s = *reinterpret_cast<const float4*>(cs + 64);
-        t = CosSin{{c.x, c.y, c.z, c.w}, {s.x, s.y, s.z, s.w}};
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const int pair = 4 * l + j;
-          const int axis = static_cast<int>(p.pair_axis[pair >> 5] >> (2 * (pair & 31))) & 3;
-          const int at = axis == 0 ? axis_pos[0] : axis == 1 ? axis_pos[1] : axis == 2 ? axis_pos[2] : axis_pos[3];
-          const float* cs = p.cos_sin + int64_t(at) * kHeadDim + pair;
-          t.c[j] = cs[0];
-          t.s[j] = cs[64];
-        }
+      if (r < own && 2 * k + half < p.G) qv[k] = load_pairs(q + 2 * k * kHeadDim, l);
+  };
+  if (warp < own) ask(warp);
+  if (tid < kMaxRows) {
+    RowInfo ri{-1, 0, 0, 0, -1, 0};
+    const int i = base + tid, beyond = tid - own + 1;   // rows behind the window's last
+    if (tid < own || (own == p.window && tid < own + kSubblock - 1 && i < p.n_rows)) {
+      uint32_t bad = 0;
+      ri = find_row(p, i, axis_pos[tid], bad);
+      if (tid < own) {
+        if (h == 0) flag_error(p.err, bad);
+      } else if (ri.b < 0 || ri.at - ri.first < beyond || ri.at % kSubblock < beyond) {
+        ri.b = -1;   // not of the sub-block of the window's last row
       }
     }
-    const bool turn = p.cos_sin != nullptr;
+    info[tid] = ri;
+  }
+  __syncthreads();
+
+  for (int r = warp; r < kMaxRows; r += n_warps) {
+    const RowInfo ri = info[r];
+    if (r >= own && ri.b < 0) break;
+    if (r != warp || r >= own) ask(r);
+    const int64_t i = base + r;
+    CosSin t{};
+    if (turn && ri.rot) {
+      if (p.n_axes == 1) {
+        const float* cs = p.cos_sin + int64_t(axis_pos[r][0]) * kHeadDim + 4 * l;
+        const float4 c = *reinterpret_cast<const float4*>(cs), s = *reinterpret_cast<const float4*>(cs + 64);
+        t.c[0] = make_float2(c.x, c.y), t.c[1] = make_float2(c.z, c.w);
+        t.s[0] = make_float2(s.x, s.y), t.s[1] = make_float2(s.z, s.w);
+      } else {
+        float c[4], s[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const int pr = 4 * l + j;
+          const int axis = static_cast<int>(p.pair_axis[pr >> 5] >> (2 * (pr & 31))) & 3;
+          const float* cs = p.cos_sin + int64_t(axis_pos[r][axis]) * kHeadDim + pr;
+          c[j] = cs[0];
+          s[j] = cs[64];
+        }
+        t.c[0] = make_float2(c[0], c[1]), t.c[1] = make_float2(c[2], c[3]);
+        t.s[0] = make_float2(s[0], s[1]), t.s[1] = make_float2(s[2], s[3]);
+      }
+    }
     // ---- query heads
     if (r < own && ri.rot) {
-      for (int k0 = 0; 2 * k0 < p.G; k0 += kHeads) {
+      const uint16_t* q = p.q + i * p.q_stride + (h * p.G + half) * kHeadDim;
+      uint16_t* to = p.q_out + (i * p.Hq + h * p.G + half) * kHeadDim;
+      for (int g = half; g < p.G; g += 2 * kHeads, q += 2 * kHeads * kHeadDim, to += 2 * kHeads * kHeadDim) {
 #pragma unroll
         for (int k = 0; k < kHeads; ++k) {
-          const int g = 2 * (k0 + k) + half;
-          if (g >= p.G) continue;
-          if (k0 > 0) qv[k] = load_pairs(q + g * kHeadDim, l);
+          if (g + 2 * k >= p.G) break;
+          if (g >= 2 * kHeads) qv[k] = load_pairs(q + 2 * k * kHeadDim, l);
           float x[8];
           rotate(qv[k], t, true, x);
-          store_pairs(p.q_out + (i * p.Hq + int64_t(h) * p.G + g) * kHeadDim, l, x);
+          store_pairs(to + 2 * k * kHeadDim, l, round_pairs(x));
         }
       }
     }
@@ -175,7 +203,8 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
       if (half == 0) {
         rotate(kv, t, turn, x);
         uint16_t* row = reinterpret_cast<uint16_t*>(p.pool) + (ph * kPageTokens + tok) * kHeadDim;
-        const uint4 v = store_pairs(r < own ? row : nullptr, l, x);
+        const uint4 v = round_pairs(x);
+        if (r < own) store_pairs(row, l, v);
         *reinterpret_cast<float4*>(&rows[r][4 * l]) =
             make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
         *reinterpret_cast<float4*>(&rows[r][64 + 4 * l]) =
@@ -233,35 +262,47 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
 
   // ---- sums of the sub-blocks whose first new row is one of this window's, 128 threads each
   const int d = tid % kHeadDim, groups = blockDim.x / kHeadDim;
-  int seen = 0;
-  for (int j = 0; j < own; ++j) {
+  unsigned turned, owners;   // rows that are in the cache; rows that are their sub-block's first new one
+  {
+    const RowInfo r = info[min(lane, kMaxRows - 1)];
+    const bool in = lane < kMaxRows && r.b >= 0 && r.phys >= 0;
+    turned = __ballot_sync(0xffffffffu, in && r.rot);
+    owners = __ballot_sync(0xffffffffu, in && lane < own && (r.at % kSubblock == 0 || r.at == r.first));
+  }
+  for (int n = 0; owners; owners &= owners - 1, ++n) {
+    if (n % groups != tid / kHeadDim) continue;
+    const int j = __ffs(owners) - 1;
     const RowInfo r = info[j];
-    if (r.b < 0 || r.phys < 0 || !(r.at % kSubblock == 0 || r.at == r.first)) continue;
-    if (seen++ % groups != tid / kHeadDim) continue;
     const int64_t ph = int64_t(h) * p.n_phys + r.phys;
     const int s0 = r.at / kSubblock * kSubblock, s1 = min(r.end, s0 + kSubblock);   // new: [r.at, s1)
-    const int cnt = max(0, min(kPageTokens, p.page_cnt[r.phys]));
-    // the rows held before, all asked for before the first is added
-    float v[kSubblock];
+    const unsigned fresh = (1u << (s1 - s0)) - (1u << (r.at - s0)), got = (turned >> j) << (r.at - s0) & fresh;
+    float sum = 0.f;
+    if (got == 0xFFFFu) {
 #pragma unroll
-    for (int k = 0; k < kSubblock; ++k) {
-      const int t = s0 + k, tok = t % kPageTokens;
-      const bool fresh = t >= r.at && t < s1;
-      v[k] = 0.f;
-      if (!fresh && tok < cnt) {
-        if (Q4) {
-          const uint8_t* page = p.pool + ph * kQ4Page;
-          v[k] = e2m1_to_f32(page[q4_k_code(tok) + d / 2] >> (4 * (d & 1))) * e4m3_to_f32(page[q4_k_scale(tok, d / kQ4Block)]);
-        } else {
-          v[k] = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(p.pool)[(ph * kPageTokens + tok) * kHeadDim + d]) << 16);
+      for (int k = 0; k < kSubblock; ++k) sum += rows[j + k][d];
+    } else {
+      // the rows held before, all asked for before the first is added
+      const int cnt = max(0, min(kPageTokens, p.page_cnt[r.phys]));
+      float v[kSubblock];
+#pragma unroll
+      for (int k = 0; k < kSubblock; ++k) {
+        const int tok = s0 % kPageTokens + k;
+        v[k] = 0.f;
+        if (got >> k & 1) {
+          v[k] = rows[j + s0 + k - r.at][d];
+        } else if (!(fresh >> k & 1) && tok < cnt) {
+          if (Q4) {
+            const uint8_t* page = p.pool + ph * kQ4Page;
+            v[k] = e2m1_to_f32(page[q4_k_code(tok) + d / 2] >> (4 * (d & 1))) * e4m3_to_f32(page[q4_k_scale(tok, d / kQ4Block)]);
+          } else {
+            v[k] = __uint_as_float(uint32_t(reinterpret_cast<const uint16_t*>(p.pool)[(ph * kPageTokens + tok) * kHeadDim + d]) << 16);
+          }
         }
-      } else if (fresh && info[j + t - r.at].rot) {
-        v[k] = rows[j + t - r.at][d];
       }
-    }
-    float sum = 0.f;   // a row that is not there adds +0, which changes no sum of this order
+      // a row that is not there adds +0, which changes no sum of this order
 #pragma unroll
-    for (int k = 0; k < kSubblock; ++k) sum += v[k];
+      for (int k = 0; k < kSubblock; ++k) sum += v[k];
+    }
     if (Q4) sum = __fmul_rn(sum, gk);
     const int64_t at = (ph * kNSub + (s0 % kPageTokens) / kSubblock) * kHeadDim + d;
     if (p.ksum_bf16) reinterpret_cast<__nv_bfloat16*>(p.ksum)[at] = __float2bfloat16_rn(sum);
