@@ -279,8 +279,10 @@ int paged_kv_append_rope(spkv_cache_t c, const void* k_new, int64_t k_stride, co
         rope->n_pos >= (int64_t(1) << 31) || (rope->n_axes > 1 && (!rope->pos || !rope->pair_axis)))
       return SPKV_EINVAL;
     p.n_axes = rope->n_axes;
+    p.quads = 1;
     for (int j = 0; rope->n_axes > 1 && j < 64; ++j) {
       if (rope->pair_axis[j] >= rope->n_axes) return SPKV_EINVAL;
+      if (rope->pair_axis[j] != rope->pair_axis[j & ~3]) p.quads = 0;
       p.pair_axis[j >> 5] |= static_cast<uint64_t>(rope->pair_axis[j]) << (2 * (j & 31));
     }
     p.pos = rope->pos;

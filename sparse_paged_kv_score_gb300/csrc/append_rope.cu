@@ -18,7 +18,7 @@ namespace {
 
 constexpr int kMaxWindow = 16;
 constexpr int kMaxRows = kMaxWindow + kSubblock - 1;
-constexpr int kHeads = 4;   // query heads of a half-warp whose rows are asked for together
+constexpr int kHeads = 2;   // query heads of a half-warp whose rows are asked for together
 
 struct RowInfo {
   int b;        // request, -1: no request's row
@@ -110,8 +110,10 @@ __device__ __forceinline__ void store_pairs(uint16_t* row, int l, uint4 v) {
   *reinterpret_cast<uint2*>(row + 64 + 4 * l) = make_uint2(v.z, v.w);
 }
 
+// Five CTAs of 256 threads an SM (48 registers): 8192 rows of 32 + 2 x 8 heads in 47 us, 49 with four, 49 with six
+// (which spill), 59 with CTAs of 512.
 template <bool Q4>
-__global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
+__global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
   __shared__ RowInfo info[kMaxRows];
   __shared__ int axis_pos[kMaxRows][4];
   __shared__ __align__(16) float rows[kMaxRows][kHeadDim];   // the cache's values of the new keys (4-bit: without g)
@@ -121,7 +123,7 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
   const int n_warps = blockDim.x >> 5;
   const int h = blockIdx.y, base = blockIdx.x * p.window;
   const int own = min(p.window, p.n_rows - base);
-  const float gk = Q4 ? p.k_scale[h] : 1.f, gv = Q4 ? p.v_scale[h] : 1.f;
+  const float gk = Q4 ? p.k_scale[h] : 1.f;
   const bool turn = p.cos_sin != nullptr;
 
   // ---- the first row's key, value and query heads are on their way while the rows' places are looked up
@@ -159,8 +161,9 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
     const int64_t i = base + r;
     CosSin t{};
     if (turn && ri.rot) {
-      if (p.n_axes == 1) {
-        const float* cs = p.cos_sin + int64_t(axis_pos[r][0]) * kHeadDim + 4 * l;
+      if (p.quads) {   // pairs 4l .. 4l + 3 of one axis
+        const int axis = static_cast<int>(p.pair_axis[l >> 3] >> (8 * (l & 7))) & 3;
+        const float* cs = p.cos_sin + int64_t(axis_pos[r][axis]) * kHeadDim + 4 * l;
         const float4 c = *reinterpret_cast<const float4*>(cs), s = *reinterpret_cast<const float4*>(cs + 64);
         t.c[0] = make_float2(c.x, c.y), t.c[1] = make_float2(c.z, c.w);
         t.s[0] = make_float2(s.x, s.y), t.s[1] = make_float2(s.z, s.w);
@@ -233,10 +236,10 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
     m1 = max(m1, __shfl_xor_sync(0xffffffffu, m1, 1));
     const uint32_t n0 = __shfl_xor_sync(0xffffffffu, m0, 2), n1 = __shfl_xor_sync(0xffffffffu, m1, 2);
     if (half == 0) m0 = max(m0, n0), m1 = max(m1, n1);
-    const float g = half == 0 ? gk : gv;
-    const uint32_t s0 = q4_scale_byte(m0, g), s1 = q4_scale_byte(m1, g);
+    const float f = half == 0 ? gk : p.v_scale[h];
+    const uint32_t s0 = q4_scale_byte(m0, f), s1 = q4_scale_byte(m1, f);
     const float e0 = e4m3_to_f32(s0), e1 = e4m3_to_f32(s1);
-    const uint32_t c0 = q4_codes(y0, __fmul_rn(e0, g)), c1 = q4_codes(y1, __fmul_rn(e1, g));
+    const uint32_t c0 = q4_codes(y0, __fmul_rn(e0, f)), c1 = q4_codes(y1, __fmul_rn(e1, f));
     if (half == 1) {
       if (r < own) {
         *reinterpret_cast<uint32_t*>(page + q4_v_code(tok, l >> 1) + (l & 1) * 4) = c0 | c1 << 16;
@@ -253,10 +256,8 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
         page[q4_k_scale(tok, 4 + (l >> 2))] = static_cast<uint8_t>(s1);
       }
     }
-    *reinterpret_cast<float4*>(&rows[r][4 * l]) = make_float4(
-        e2m1_to_f32(c0) * e0, e2m1_to_f32(c0 >> 4) * e0, e2m1_to_f32(c0 >> 8) * e0, e2m1_to_f32(c0 >> 12) * e0);
-    *reinterpret_cast<float4*>(&rows[r][64 + 4 * l]) = make_float4(
-        e2m1_to_f32(c1) * e1, e2m1_to_f32(c1 >> 4) * e1, e2m1_to_f32(c1 >> 8) * e1, e2m1_to_f32(c1 >> 12) * e1);
+    *reinterpret_cast<float4*>(&rows[r][4 * l]) = q4_values(c0, e0);
+    *reinterpret_cast<float4*>(&rows[r][64 + 4 * l]) = q4_values(c1, e1);
   }
   __syncthreads();
 
@@ -281,16 +282,17 @@ __global__ void __launch_bounds__(256) append_rope_kernel(const __grid_constant_
 #pragma unroll
       for (int k = 0; k < kSubblock; ++k) sum += rows[j + k][d];
     } else {
-      // the rows held before, all asked for before the first is added
+      // the rows held before, all asked for before the first is added: those in front of the new ones, and
+      // what page_cnt (which this call raises no further than its own rows) counts behind them
       const int cnt = max(0, min(kPageTokens, p.page_cnt[r.phys]));
       float v[kSubblock];
 #pragma unroll
       for (int k = 0; k < kSubblock; ++k) {
         const int tok = s0 % kPageTokens + k;
-        v[k] = 0.f;
+        v[k] = 0.f;   // a new row that is not in the cache
         if (got >> k & 1) {
           v[k] = rows[j + s0 + k - r.at][d];
-        } else if (!(fresh >> k & 1) && tok < cnt) {
+        } else if (s0 + k < r.at || (s0 + k >= s1 && tok < cnt)) {
           if (Q4) {
             const uint8_t* page = p.pool + ph * kQ4Page;
             v[k] = e2m1_to_f32(page[q4_k_code(tok) + d / 2] >> (4 * (d & 1))) * e4m3_to_f32(page[q4_k_scale(tok, d / kQ4Block)]);

@@ -186,6 +186,7 @@ struct AppendRopeParams {
   const float* cos_sin;          // [n_pos][128] or null: no rotation
   int64_t n_pos;
   uint64_t pair_axis[2];         // two bits a pair
+  int quads;                     // pairs 4l .. 4l + 3 have one axis, for every l
   int window;                    // rows per CTA (set by the launch)
   uint8_t* pool;                 // key pool (bf16) or the 4-bit pool
   uint8_t* v_pool;               // bf16 form

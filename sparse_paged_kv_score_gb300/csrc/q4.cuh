@@ -99,4 +99,13 @@ __device__ __forceinline__ uint32_t q4_codes(const float (&x)[N], float d) {
   return w;
 }
 
+// Four codes (the low 16 bits of c) times their scale, exact.
+__device__ __forceinline__ float4 q4_values(uint32_t c, float scale) {
+  uint32_t h[4];
+  e2m1_to_f16(c, h);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&h[0]));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&h[1]));
+  return make_float4(a.x * scale, a.y * scale, b.x * scale, b.y * scale);
+}
+
 }  // namespace spkv

@@ -94,6 +94,10 @@ class Batch:
                 self.cnt[p] = max(self.cnt[p], t + 1)
         return q_out
 
+    def expect_none(self):
+        """After a call whose rows are no request's: as the call before left it."""
+        return host_bits(self.q_out)
+
     def check(self, q_out):
         assert np.array_equal(self.cnt_d.cpu().numpy(), self.cnt)
         if self.q4:
@@ -291,7 +295,6 @@ def test_prompt_then_decode_on_a_q4_cache(steps):
     """Prompts, then decode steps: append, block scores, selection, attention, all on the 4-bit cache."""
     Hq, Hk, B = 8, 2, 3
     b = Batch(True, [0, 0, 0], [300, 64, 131], Hq, Hk, seed=14)
-    pad = np.full((B, 4), b.n_phys, np.int32)
     b.call()
     q = b.expect()
     b.check(q)
@@ -299,7 +302,6 @@ def test_prompt_then_decode_on_a_q4_cache(steps):
     alive = torch.full((B, Hk, (npm + 31) // 32), -1, dtype=torch.int32, device=DEV)
     rng = np.random.default_rng(1)
     ev = f32(rng.standard_normal((B, Hk, npm)))
-    assert pad.shape[0] == B
     for step in range(steps):
         w = ref.bf16(rng.standard_normal((B, Hq + 2 * Hk, 128)))
         b.x, b.n, b.lens = w, B, np.ones(B, int)
@@ -370,3 +372,91 @@ def test_unpacked_pages_feed_the_prefill():
                 want = p @ vv / p.sum()
                 dx = 2.0 ** -7 * (np.abs(kk) @ np.abs(r)).max() / np.sqrt(128)
                 assert np.abs(out[0, t, g].cpu().numpy() - want).max() <= 2 * (dx + 2.0 ** -7) * np.abs(vv).max()
+
+
+@pytest.mark.parametrize("q4", FORMATS)
+def test_rows_in_front_count_as_held(q4):
+    """A page whose count is behind the request's first new row: the rows in front are summed, as
+    paged_kv_append sums them; what a count tells behind the last new row is summed too."""
+    b = Batch(q4, [37, 100], [6, 2], 4, 2, seed=16)
+    b.cnt[b.pt[0, 0]], b.cnt[b.pt[1, 1]] = 3, 45    # request 1's new rows are 36 and 37 of its page
+    b.cnt_d.copy_(i32(b.cnt))
+    b.call()
+    b.check(b.expect())
+
+
+@pytest.mark.parametrize("q4", FORMATS)
+def test_rows_of_no_request(q4):
+    """Rows before the first request, empty requests, and a call of nothing."""
+    b = Batch(q4, [0, 9, 64], [5, 0, 4], 4, 2, seed=17, pad=6)
+    b.first = b.first + 3      # rows 0 .. 2 and the last three belong to no request
+    b.call()
+    assert spkv.get_device_error(b.cache) == (0, 0)
+    b.check(b.expect())
+    b.call(row_first=i32([3, 3, 3, 3]))
+    b.check(b.expect_none())
+    none = torch.empty(0, 2, 128, dtype=torch.bfloat16, device=DEV)
+    spkv.paged_kv_append_rope(b.cache, none, none, i32(np.zeros(0)), i32(np.zeros((0, 4))))
+
+
+def test_two_handles_in_two_graphs():
+    """Each handle has its own workspace: graphs of two, replayed on two streams at once."""
+    caches = [Batch(q4, [40, 3], [1, 1], 8, 2, seed=18 + q4) for q4 in (True, False)]
+    graphs = []
+    keep = []
+    for b in caches:
+        a = i32(b.L), i32(b.pt)
+        kw = dict(row_first=i32(b.first), q=b.qd, q_out=b.q_out, cos_sin=f32(b.tab))
+        keep.append((a, kw))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            spkv.paged_kv_append_rope(b.cache, b.kd, b.vd, *a, **kw)
+        graphs.append(g)
+    streams = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for g, s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for b in caches:
+        b.check(b.expect())
+
+
+def test_refused_arguments():
+    b = Batch(True, [5, 7], [1, 1], 8, 2, seed=19)
+    wide = torch.zeros(2, 3, 130, dtype=torch.bfloat16, device=DEV)
+    L, pt, tab = i32(b.L), i32(b.pt), f32(b.tab)
+    rot = dict(q=b.qd, q_out=b.q_out, cos_sin=tab)
+
+    def refused(error, *, k=b.kd, v=b.vd, L=L, pt=pt, cache=b.cache, **kw):
+        with pytest.raises(error) as e:
+            spkv.paged_kv_append_rope(cache, k, v, L, pt, **kw)
+        return e.value
+
+    E, A = ValueError, spkv.SpkvError
+    refused(E, k=wide[:, :2, :128])                                  # heads apart
+    refused(E, k=b.kd[:1])                                           # another number of rows
+    assert refused(A, k=b.kd[:1].expand(2, 2, 128)).status == -1     # one row for all
+    odd = torch.zeros(2, 2 * 128 + 4, dtype=torch.bfloat16, device=DEV)[:, :256].view(2, 2, 128)
+    assert refused(A, v=odd).status == -1                            # rows 8 bytes off
+    assert refused(A, k=torch.zeros(2 * 256 + 4, dtype=torch.bfloat16, device=DEV)[4:].view(2, 2, 128)).status == -1
+    assert refused(A, L=L[:1], pt=pt[:1]).status == -1               # two rows, one request, no row_first
+    refused(E, q=b.qd, q_out=b.q_out)                                # queries are rotated or not given
+    refused(E, q=b.qd, cos_sin=tab)                                  # nowhere to write them
+    refused(E, pos=i32([1, 2]))
+    refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]))               # which axis turns which pair?
+    refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[0] * 63)
+    refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[2] * 64)
+    assert refused(A, cos_sin=tab, pos=i32(np.zeros((2, 5))), pair_axis=[4] * 64).status == -1   # five axes
+    assert refused(A, q=b.qd[:, :7].contiguous(), q_out=b.q_out[:, :7].contiguous(), cos_sin=tab).status == -1
+    many = torch.zeros(2, 34, 128, dtype=torch.bfloat16, device=DEV)
+    assert refused(A, q=many, q_out=many, cos_sin=tab).status == -6  # more than 16 heads a group
+    assert refused(A, pt=pt[:, :0], **rot).status == -1              # a table of no pages
+    refused(TypeError, q=b.qd.half(), q_out=b.q_out, cos_sin=tab)
+    refused(TypeError, L=L.long())
+    bare = spkv.paged_kv_create_q4(b.pool, f32(b.gk), f32(b.gv), None, None, max_units=4)
+    assert refused(A, cache=bare, **rot).status == -1                # no sums to keep
+    assert spkv.get_device_error(b.cache) == (0, 0)
+    b.call(**rot)
+    b.check(b.expect())
