@@ -248,11 +248,11 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
         if q_out is None:
             raise ValueError("q_out: needed with q")
         qo = _t(q_out, torch.bfloat16, "q_out", (n, Hq, HEAD_DIM))
+    first = None if row_first is None else _t(row_first, torch.int32, "row_first", (B + 1,))
+    lens, table = _t(seq_len, torch.int32, "seq_len", (B,)), _t(page_table, torch.int32, "page_table", (B, np_max))
     with _on(dev):
         check("paged_kv_append_rope", load().paged_kv_append_rope(
-            cache.handle, kp, ks, vp, vs, n, B, None if row_first is None else _t(row_first, torch.int32, "row_first", (B + 1,)),
-            _t(seq_len, torch.int32, "seq_len", (B,)), _t(page_table, torch.int32, "page_table", (B, np_max)), np_max,
-            rope, qp, qs, Hq, qo, _stream(stream)))
+            cache.handle, kp, ks, vp, vs, n, B, first, lens, table, np_max, rope, qp, qs, Hq, qo, _stream(stream)))
 
 
 def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
@@ -262,10 +262,10 @@ def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
     shp = (cache.n_kv_heads, n, PAGE, HEAD_DIM)
     dev = cache.tensors[0].device
     _same_device(dev, pages=pages, k_out=k_out, v_out=v_out)
+    args = (_t(pages, torch.int32, "pages", (n,)), n, _t(k_out, torch.bfloat16, "k_out", shp),
+            _t(v_out, torch.bfloat16, "v_out", shp))
     with _on(dev):
-        check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(
-            cache.handle, _t(pages, torch.int32, "pages", (n,)), n, _t(k_out, torch.bfloat16, "k_out", shp),
-            _t(v_out, torch.bfloat16, "v_out", shp), _stream(stream)))
+        check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(cache.handle, *args, _stream(stream)))
 
 
 def paged_kv_append(cache: PagedKVCache, phys_page, tok_in_page, k_new, v_new, stream=None):

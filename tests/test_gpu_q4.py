@@ -369,3 +369,44 @@ def test_refused_calls():
                                 torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV))
     assert e.value.status == U
     assert spkv.get_device_error(c.handle) == (0, 0)
+
+
+def test_wait_limit_then_recovery():
+    """With no time to wait a call may give up (status and flag, nothing else), the next one is right again."""
+    c = Cache(2, 3, 60, [60 * 64, 64 * 60 - 5, 700], seed=20)
+    x, q = queries(3, 8)
+    sel, n = c.select(48, np.random.default_rng(0))
+    c.handle.set_wait_limit(0)
+    for _ in range(3):
+        c.attend(q, sel, n)
+        st, bits = spkv.get_device_error(c.handle)
+        assert (st, bits) in ((0, 0), (-5, spkv.DEVERR["TIMEOUT"]))
+    c.handle.set_wait_limit(1_000_000_000)
+    for _ in range(2):
+        out, lse = c.attend(q, sel, n)
+        assert spkv.get_device_error(c.handle) == (0, 0)
+        check(out, lse, ref.attention(x, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
+
+
+def test_two_handles_in_two_graphs():
+    """Two caches' attention captured, and replayed on two streams at once: each has its own workspace."""
+    work = []
+    for seed in (21, 22):
+        c = Cache(2, 2, 150, [9600, 9001], seed=seed)
+        x, q = queries(2, 8, seed=seed)
+        sel, n = c.select(140, np.random.default_rng(seed))
+        d = i32(c.pt), i32(sel), i32(n), i32(c.L)
+        out, lse = torch.zeros(2, 8, 128, device=DEV), torch.zeros(2, 8, device=DEV)
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            spkv.sparse_decode_attn(c.handle, q, *d, out, lse)
+        work.append((c, x, q, sel, n, d, out, lse, g, torch.cuda.Stream()))
+    for _ in range(10):
+        for w in work:
+            with torch.cuda.stream(w[9]):
+                w[8].replay()
+    torch.cuda.synchronize()
+    for c, x, q, sel, n, d, out, lse, g, s in work:
+        assert spkv.get_device_error(c.handle) == (0, 0)
+        check(out, lse, ref.attention(x, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
