@@ -196,15 +196,25 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name}: must be on {device}, the cache's device")
 
 
-def _rows(x: torch.Tensor, name: str, n: int, heads: int):
-    """Address and row stride of bf16 rows [n][heads][128] whose rows may lie apart (a slice of a
+def _on_device(x: torch.Tensor, dtype, name: str, shape, device) -> int:
+    """_t of a tensor on ``device``; one look at its index, where the rest is as it should be."""
+    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == device.index and x.is_contiguous()
+            and x.shape == shape):
+        return x.data_ptr()
+    at = _t(x, dtype, name, shape)
+    _same_device(device, **{name: x})
+    return at
+
+
+def _rows(x: torch.Tensor, name: str, n: int, heads: int, device):
+    """Address and row stride of bf16 rows [n][heads][128] on ``device`` whose rows may lie apart (a slice of a
     wider projection's output)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {x.dtype}")
-    if not x.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor")
+    if x.get_device() != device.index or not x.is_cuda:
+        raise ValueError(f"{name}: must be a CUDA tensor on {device}, the cache's device")
     if x.shape != (n, heads, HEAD_DIM):
         raise ValueError(f"{name}: expected shape {(n, heads, HEAD_DIM)}, got {tuple(x.shape)}")
     row, head, one = x.stride()
@@ -223,10 +233,8 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
     n, Hk = k_new.shape[0], cache.n_kv_heads
     B, np_max = page_table.shape
     dev = cache.tensors[0].device
-    _same_device(dev, k_new=k_new, v_new=v_new, seq_len=seq_len, page_table=page_table, row_first=row_first, q=q,
-                 q_out=q_out, cos_sin=cos_sin, pos=pos)
-    kp, ks = _rows(k_new, "k_new", n, Hk)
-    vp, vs = _rows(v_new, "v_new", n, Hk)
+    kp, ks = _rows(k_new, "k_new", n, Hk, dev)
+    vp, vs = _rows(v_new, "v_new", n, Hk, dev)
     rope, axes, qp, qs, Hq, qo = None, None, None, 0, 0, None
     if cos_sin is not None:
         n_axes = 1 if pos is None or pos.dim() == 1 else pos.shape[1]
@@ -236,20 +244,20 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
             axes = (ctypes.c_uint8 * (HEAD_DIM // 2))(*(int(a) for a in pair_axis))
         elif n_axes > 1:
             raise ValueError("pair_axis: needed with several axes")
-        if pos is not None:
-            _t(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (n, n_axes))
-        rope = ctypes.byref(SpkvRope(_t(cos_sin, torch.float32, "cos_sin", (cos_sin.shape[0], HEAD_DIM)),
-                                     cos_sin.shape[0], n_axes, axes, None if pos is None else pos.data_ptr()))
+        n_pos = cos_sin.shape[0]
+        rope = SpkvRope(_on_device(cos_sin, torch.float32, "cos_sin", (n_pos, HEAD_DIM), dev), n_pos, n_axes, axes, None if pos is None
+                        else _on_device(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (n, n_axes), dev))
     elif pos is not None or pair_axis is not None or q is not None:
         raise ValueError("pos, pair_axis and q are given with cos_sin")
     if q is not None:
         Hq = q.shape[1]
-        qp, qs = _rows(q, "q", n, Hq)
+        qp, qs = _rows(q, "q", n, Hq, dev)
         if q_out is None:
             raise ValueError("q_out: needed with q")
-        qo = _t(q_out, torch.bfloat16, "q_out", (n, Hq, HEAD_DIM))
-    first = None if row_first is None else _t(row_first, torch.int32, "row_first", (B + 1,))
-    lens, table = _t(seq_len, torch.int32, "seq_len", (B,)), _t(page_table, torch.int32, "page_table", (B, np_max))
+        qo = _on_device(q_out, torch.bfloat16, "q_out", (n, Hq, HEAD_DIM), dev)
+    first = None if row_first is None else _on_device(row_first, torch.int32, "row_first", (B + 1,), dev)
+    lens = _on_device(seq_len, torch.int32, "seq_len", (B,), dev)
+    table = _on_device(page_table, torch.int32, "page_table", (B, np_max), dev)
     with _on(dev):
         check("paged_kv_append_rope", load().paged_kv_append_rope(
             cache.handle, kp, ks, vp, vs, n, B, first, lens, table, np_max, rope, qp, qs, Hq, qo, _stream(stream)))
@@ -261,9 +269,8 @@ def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
     n = pages.shape[0]
     shp = (cache.n_kv_heads, n, PAGE, HEAD_DIM)
     dev = cache.tensors[0].device
-    _same_device(dev, pages=pages, k_out=k_out, v_out=v_out)
-    args = (_t(pages, torch.int32, "pages", (n,)), n, _t(k_out, torch.bfloat16, "k_out", shp),
-            _t(v_out, torch.bfloat16, "v_out", shp))
+    args = (_on_device(pages, torch.int32, "pages", (n,), dev), n, _on_device(k_out, torch.bfloat16, "k_out", shp, dev),
+            _on_device(v_out, torch.bfloat16, "v_out", shp, dev))
     with _on(dev):
         check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(cache.handle, *args, _stream(stream)))
 

@@ -375,6 +375,9 @@ struct Cfg {
   static_assert(L % NS == 0 && L % TEAMS == 0, "barriers");
 };
 
+constexpr int kCtaPages = 8;    // pages of a CTA, at least
+constexpr int kPartPages = 4;   // and of one that takes a part of a unit
+
 template <int CG, bool PACK>
 struct SmemQ4 {
   using C = Cfg<CG, PACK>;
@@ -477,6 +480,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   };
   // ---- this CTA's pages [x0, x1) of T; the window of units for the look-ups, and its first page
   int x0, x1, base_u = 0, base_x = 0;
+  int unit_parts = 1;
   int share = 1, extra = 0;   // pages of a CTA, and how many CTAs take one more
   auto cta_begin = [&](int c) { return c * share + min(c, extra); };
   auto cta_of = [&](int x) {
@@ -497,10 +501,11 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   if (BY_UNIT) {
     base_u = cta / p4.parts;
     const int n = count(base_u), part = cta % p4.parts;
-    x0 = static_cast<int>(int64_t(n) * part / p4.parts);
-    x1 = static_cast<int>(int64_t(n) * (part + 1) / p4.parts);
+    unit_parts = min(p4.parts, (n + kPartPages - 1) / kPartPages);
     if (part == 0 && n == 0) write_empty(base_u);
-    if (x0 == x1) return;
+    if (part >= unit_parts) return;
+    x0 = n * part / unit_parts;   // (3 SMs CTAs of 4 pages at most: no overflow)
+    x1 = n * (part + 1) / unit_parts;
     if (tid == 0) S.first[0] = 0;
     for (int i = tid; i < C::kWindow; i += C::kThreads) S.first[i + 1] = n;
     __syncthreads();
@@ -538,6 +543,16 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   int cur = -1;        // the unit that the warps' states are of
   bool head = true;    // whether it is the CTA's first
   bool ok = true;
+  auto take = [&](int u) {   // the warps' states become those of unit u
+    const int64_t row = row_of(u);
+    if (tid == 0) {
+      S.row = row;
+      S.gv = p4.v_scale[u % p.Hk];
+    }
+    w.load_q(static_cast<const uint16_t*>(p.q) + (row + c8) * kHeadDim, p.G - c8, p.scale_log2 * p4.k_scale[u % p.Hk], lane);
+    w.reset();
+    cur = u;
+  };
   for (int x = x0; x < x1;) {
     // ---- as many pages as there are descriptors, and as the window has
     const int end = min(x1, S.first[C::kWindow]);   // of the pages in the window
@@ -563,21 +578,21 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       if (tid < NS && ok) copy(tid, d);
       S.desc[tid] = d;
     }
+    if (cur < 0 && cnt > 0) {   // the first unit's queries come while the other threads look up
+      int su = 0;
+#pragma unroll
+      for (int o = C::kWindow / 2; o > 0; o >>= 1)
+        if (S.first[su + o] <= x) su += o;
+      take(base_u + su);
+    }
     __syncthreads();
     for (int kb = 0; kb < cnt;) {
       // ---- a segment: descriptors [kb, ke)
       const int su = S.desc[kb].y >> 8, u = base_u + su;
       const int f = S.first[su], e = S.first[su + 1], ke = min(cnt, e - x);
       if (u != cur) {
-        const int64_t row = row_of(u);
-        if (tid == 0) {
-          S.row = row;
-          S.gv = p4.v_scale[u % p.Hk];
-        }
-        w.load_q(static_cast<const uint16_t*>(p.q) + (row + c8) * kHeadDim, p.G - c8, p.scale_log2 * p4.k_scale[u % p.Hk], lane);
-        w.reset();
-        head = cur < 0;
-        cur = u;
+        take(u);
+        head = false;
       }
       for (int i = kb + (team + TEAMS - (j0 + kb) % TEAMS) % TEAMS; i < ke && ok; i += TEAMS) {
         const int j = j0 + i, s = j % NS;
@@ -601,6 +616,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       if (x + ke < min(e, x1)) break;   // it goes on with the next descriptors
       // ---- its end: the teams' states merged, a warp taking a query head at a time
       w.store(S.state[team], c8, lane);
+      w.reset();   // nothing of it is kept over the merges
       const bool whole = f >= x0 && e <= x1;
       __syncthreads();
       const int64_t row = S.row;
@@ -634,54 +650,70 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       if (whole) continue;
       // ---- a unit of several CTAs: the last to arrive merges
       const int c0 = BY_UNIT ? cta - cta % p4.parts : cta_of(f);
-      const int parts = BY_UNIT ? p4.parts : cta_of(e - 1) - c0 + 1;
+      const int parts = BY_UNIT ? unit_parts : cta_of(e - 1) - c0 + 1;
       const int late = !BY_UNIT && f > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
-      const int held = BY_UNIT ? min(e, parts) : parts;         // parts with pages
       if (tid == 0) {
         int before;   // release: this CTA's part, which the barrier has ordered before; acquire: the others'
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.ws_parts + u) : "memory");
-        S.last = before == held - 1;
+        S.last = before == parts - 1;
         if (S.last) p.ws_parts[u] = 0;
       }
       __syncthreads();
       if (S.last) {
-        for (int g = warp; g < p.G; g += C::W) {
-          float M = -CUDART_INF_F, sum = 0.f;
-          float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-          constexpr int kBatch = 8;
-          for (int i0 = 0; i0 < parts; i0 += kBatch) {
-            float m[kBatch], l[kBatch];
-            float4 o[kBatch];
+        // A warp's heads together, kBatch parts at a time: all their rows are asked for before the first is
+        // used.  Lane i has part i's reference and sum.
+        constexpr int HG = (C::kCols + C::W - 1) / C::W, kBatch = HG == 4 ? 8 : 16;
+        float M[HG], sum[HG];
+        float4 acc[HG];
 #pragma unroll
-            for (int q = 0; q < kBatch; ++q) {
-              m[q] = -CUDART_INF_F;
-              l[q] = 0.f;
-              o[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-              const int i = i0 + q;
-              if (i < parts && (!BY_UNIT || int64_t(e) * i / parts < int64_t(e) * (i + 1) / parts)) {
-                const int c = c0 + i;   // the unit is its CTA's first, but perhaps where it begins
-                const int64_t at = (BY_UNIT ? c : 2 * c + (i == 0 ? late : 0)) * 16 + g;
-                m[q] = __ldcg(p.ws_m + at);
-                l[q] = __ldcg(p.ws_l + at);
-                o[q] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + at * kHeadDim) + lane);
-              }
+        for (int k = 0; k < HG; ++k) M[k] = -CUDART_INF_F, sum[k] = 0.f, acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        auto place = [&](int i, int k) {   // the unit is its CTA's first, but perhaps where it begins
+          const int c = c0 + i;
+          return int64_t(BY_UNIT ? c : 2 * c + (i == 0 ? late : 0)) * 16 + warp + C::W * k;
+        };
+        for (int i0 = 0; i0 < parts; i0 += kBatch) {
+          float m[HG], l[HG];
+          float4 o[HG][kBatch];
+#pragma unroll
+          for (int k = 0; k < HG; ++k) {
+            const bool some = warp + C::W * k < p.G;
+            m[k] = -CUDART_INF_F;
+            l[k] = 0.f;
+            if (some && lane < kBatch && i0 + lane < parts) {
+              m[k] = __ldcg(p.ws_m + place(i0 + lane, k));
+              l[k] = __ldcg(p.ws_l + place(i0 + lane, k));
             }
-            float mb = M;
-#pragma unroll
-            for (int q = 0; q < kBatch; ++q) mb = fmaxf(mb, m[q]);
-            const float f0 = M == mb ? 1.f : exp2f(M - mb);
-            sum *= f0;
-            acc.x *= f0, acc.y *= f0, acc.z *= f0, acc.w *= f0;
-            M = mb;
 #pragma unroll
             for (int q = 0; q < kBatch; ++q) {
-              const float f = m[q] == M ? 1.f : exp2f(m[q] - M);   // -inf: 0, or 1 times a zero (or NaN) state
-              sum += f * l[q];
-              acc.x += f * o[q].x, acc.y += f * o[q].y, acc.z += f * o[q].z, acc.w += f * o[q].w;
+              o[k][q] = make_float4(0.f, 0.f, 0.f, 0.f);
+              if (some && i0 + q < parts)
+                o[k][q] = __ldcg(reinterpret_cast<const float4*>(p.ws_o + place(i0 + q, k) * kHeadDim) + lane);
             }
           }
-          write_row(p, row + g, lane, M, sum, acc, gv);
+#pragma unroll
+          for (int k = 0; k < HG; ++k) {
+            float mb = fmaxf(M[k], m[k]);
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) mb = fmaxf(mb, __shfl_xor_sync(0xffffffffu, mb, x));
+            const float f0 = M[k] == mb ? 1.f : exp2f(M[k] - mb);
+            const float f = m[k] == mb ? 1.f : exp2f(m[k] - mb);   // -inf: 0, or 1 times a zero (or NaN) state
+            M[k] = mb;
+            float s = f * l[k];
+#pragma unroll
+            for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
+            sum[k] = sum[k] * f0 + s;
+            acc[k].x *= f0, acc[k].y *= f0, acc[k].z *= f0, acc[k].w *= f0;
+#pragma unroll
+            for (int q = 0; q < kBatch; ++q) {
+              const float fq = __shfl_sync(0xffffffffu, f, q);
+              acc[k].x += fq * o[k][q].x, acc[k].y += fq * o[k][q].y;
+              acc[k].z += fq * o[k][q].z, acc[k].w += fq * o[k][q].w;
+            }
+          }
         }
+#pragma unroll
+        for (int k = 0; k < HG; ++k)
+          if (warp + C::W * k < p.G) write_row(p, row + warp + C::W * k, lane, M[k], sum[k], acc[k], gv);
       }
     }
     if (__syncthreads_or(!ok)) ok = false;   // the descriptors and the window are free again
@@ -703,9 +735,6 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   // no copy is left in flight (with the full limit: copies end in microseconds)
   if (tid < NS && S.copied[tid] >= 0) mbar_wait(&S.full[S.copied[tid] % L], (S.copied[tid] / L) & 1);
 }
-
-constexpr int kCtaPages = 8;    // pages of a CTA, at least
-constexpr int kPartPages = 4;   // and of one that takes a part of a unit
 
 template <int CG, bool PACK>
 cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
