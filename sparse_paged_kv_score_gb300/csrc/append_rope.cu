@@ -8,8 +8,8 @@
 // One CTA takes `window` consecutive rows of one kv head, a warp a row at a time: the lower half-warp its
 // key, the upper its value, then each half a query head (lane l of 16 holds dims 4l .. 4l + 3 and 64 + 4l ..
 // + 3, so both halves of every pair).  The rows are asked for before their places are looked up.  A
-// row's sub-block is summed by the CTA that holds its first new row; the at most 15 rows of it that lie in
-// the next window are rotated again there, so no CTA waits for another's rows and one launch does.
+// sub-block's keys and values, and its sums, are the CTA's that holds its first new row, with the at most
+// 15 rows of it that lie behind the window, so no CTA waits for another's rows and one launch does.
 #include "q4.cuh"
 #include "summary.cuh"
 
@@ -25,7 +25,7 @@ struct RowInfo {
   int at;       // position in the request's context
   int first;    // the request's first new position
   int end;      // one past its last
-  int phys;     // physical page, -1: not appended
+  int phys;     // physical page, -1: not appended, or not by this CTA
   int rot;      // positions within the table
 };
 
@@ -128,27 +128,26 @@ __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_consta
 
   // ---- the first row's key, value and query heads are on their way while the rows' places are looked up
   uint4 kv, qv[kHeads];
-  auto ask = [&](int r) {
+  auto ask = [&](int r, bool cached) {
     const int64_t i = base + r;
-    kv = half == 0 ? load_pairs(p.k_new + i * p.k_stride + h * kHeadDim, l)
-                   : *reinterpret_cast<const uint4*>(p.v_new + i * p.v_stride + h * kHeadDim + 8 * l);
+    if (cached)
+      kv = half == 0 ? load_pairs(p.k_new + i * p.k_stride + h * kHeadDim, l)
+                     : *reinterpret_cast<const uint4*>(p.v_new + i * p.v_stride + h * kHeadDim + 8 * l);
     const uint16_t* q = p.q + i * p.q_stride + (h * p.G + half) * kHeadDim;
 #pragma unroll
     for (int k = 0; k < kHeads; ++k)
       if (r < own && 2 * k + half < p.G) qv[k] = load_pairs(q + 2 * k * kHeadDim, l);
   };
-  if (warp < own) ask(warp);
+  if (warp < own) ask(warp, true);
   if (tid < kMaxRows) {
     RowInfo ri{-1, 0, 0, 0, -1, 0};
-    const int i = base + tid, beyond = tid - own + 1;   // rows behind the window's last
-    if (tid < own || (own == p.window && tid < own + kSubblock - 1 && i < p.n_rows)) {
+    if (tid < own + kSubblock - 1 && base + tid < p.n_rows) {
       uint32_t bad = 0;
-      ri = find_row(p, i, axis_pos[tid], bad);
-      if (tid < own) {
-        if (h == 0) flag_error(p.err, bad);
-      } else if (ri.b < 0 || ri.at - ri.first < beyond || ri.at % kSubblock < beyond) {
-        ri.b = -1;   // not of the sub-block of the window's last row
-      }
+      ri = find_row(p, base + tid, axis_pos[tid], bad);
+      if (tid < own && h == 0) flag_error(p.err, bad);
+      // its sub-block's first new row is one of the window's
+      const int opens = tid - min(ri.at % kSubblock, ri.at - ri.first);
+      if (opens < 0 || opens >= own) ri.b = ri.phys = -1;
     }
     info[tid] = ri;
   }
@@ -156,8 +155,8 @@ __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_consta
 
   for (int r = warp; r < kMaxRows; r += n_warps) {
     const RowInfo ri = info[r];
-    if (r >= own && ri.b < 0) break;
-    if (r != warp || r >= own) ask(r);
+    if (r >= own && ri.b < 0) break;   // nor is any row behind it
+    if (r != warp || r >= own) ask(r, ri.phys >= 0);
     const int64_t i = base + r;
     CosSin t{};
     if (turn && ri.rot) {
@@ -207,12 +206,12 @@ __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_consta
         rotate(kv, t, turn, x);
         uint16_t* row = reinterpret_cast<uint16_t*>(p.pool) + (ph * kPageTokens + tok) * kHeadDim;
         const uint4 v = round_pairs(x);
-        if (r < own) store_pairs(row, l, v);
+        store_pairs(row, l, v);
         *reinterpret_cast<float4*>(&rows[r][4 * l]) =
             make_float4(bf16lo_to_f32(v.x), bf16hi_to_f32(v.x), bf16lo_to_f32(v.y), bf16hi_to_f32(v.y));
         *reinterpret_cast<float4*>(&rows[r][64 + 4 * l]) =
             make_float4(bf16lo_to_f32(v.z), bf16hi_to_f32(v.z), bf16lo_to_f32(v.w), bf16hi_to_f32(v.w));
-      } else if (r < own) {
+      } else {
         *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.v_pool) + (ph * kPageTokens + tok) * kHeadDim + 8 * l) = kv;
       }
       continue;
@@ -241,20 +240,16 @@ __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_consta
     const float e0 = e4m3_to_f32(s0), e1 = e4m3_to_f32(s1);
     const uint32_t c0 = q4_codes(y0, __fmul_rn(e0, f)), c1 = q4_codes(y1, __fmul_rn(e1, f));
     if (half == 1) {
-      if (r < own) {
-        *reinterpret_cast<uint32_t*>(page + q4_v_code(tok, l >> 1) + (l & 1) * 4) = c0 | c1 << 16;
-        if (!(l & 1)) page[q4_v_scale(tok, l >> 1)] = static_cast<uint8_t>(s0);
-      }
+      *reinterpret_cast<uint32_t*>(page + q4_v_code(tok, l >> 1) + (l & 1) * 4) = c0 | c1 << 16;
+      if (!(l & 1)) page[q4_v_scale(tok, l >> 1)] = static_cast<uint8_t>(s0);
       continue;
     }
-    if (r < own) {
-      uint16_t* dst = reinterpret_cast<uint16_t*>(page + q4_k_code(tok));
-      dst[l] = static_cast<uint16_t>(c0);
-      dst[16 + l] = static_cast<uint16_t>(c1);
-      if (!(l & 3)) {
-        page[q4_k_scale(tok, l >> 2)] = static_cast<uint8_t>(s0);
-        page[q4_k_scale(tok, 4 + (l >> 2))] = static_cast<uint8_t>(s1);
-      }
+    uint16_t* dst = reinterpret_cast<uint16_t*>(page + q4_k_code(tok));
+    dst[l] = static_cast<uint16_t>(c0);
+    dst[16 + l] = static_cast<uint16_t>(c1);
+    if (!(l & 3)) {
+      page[q4_k_scale(tok, l >> 2)] = static_cast<uint8_t>(s0);
+      page[q4_k_scale(tok, 4 + (l >> 2))] = static_cast<uint8_t>(s1);
     }
     *reinterpret_cast<float4*>(&rows[r][4 * l]) = q4_values(c0, e0);
     *reinterpret_cast<float4*>(&rows[r][64 + 4 * l]) = q4_values(c1, e1);
@@ -310,7 +305,7 @@ __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_consta
     if (p.ksum_bf16) reinterpret_cast<__nv_bfloat16*>(p.ksum)[at] = __float2bfloat16_rn(sum);
     else reinterpret_cast<float*>(p.ksum)[at] = sum;
   }
-  if (h == 0 && tid < own) {
+  if (h == 0 && tid < kMaxRows) {
     const RowInfo r = info[tid];
     if (r.b >= 0 && r.phys >= 0 && r.rot) atomicMax(&p.page_cnt[r.phys], r.at % kPageTokens + 1);
   }
