@@ -223,6 +223,9 @@ def _rows(x: torch.Tensor, name: str, n: int, heads: int, device):
     return x.data_ptr(), row if n > 1 else heads * HEAD_DIM
 
 
+_PairAxes = ctypes.c_uint8 * (HEAD_DIM // 2)
+
+
 def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table, row_first=None, q=None, q_out=None,
                          cos_sin=None, pos=None, pair_axis=None, stream=None):
     """Appends rows k_new, v_new (bf16 [n_rows][Hk][128]; rows may be strided) to a bf16 or 4-bit cache, keys
@@ -239,9 +242,10 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
     if cos_sin is not None:
         n_axes = 1 if pos is None or pos.dim() == 1 else pos.shape[1]
         if pair_axis is not None:
-            if len(pair_axis) != HEAD_DIM // 2 or not all(0 <= int(a) < n_axes for a in pair_axis):
+            axes = bytes(pair_axis if isinstance(pair_axis, (list, tuple)) else [int(a) for a in pair_axis])
+            if len(axes) != HEAD_DIM // 2 or max(axes) >= n_axes:
                 raise ValueError(f"pair_axis: expected {HEAD_DIM // 2} axes below {n_axes}")
-            axes = (ctypes.c_uint8 * (HEAD_DIM // 2))(*(int(a) for a in pair_axis))
+            axes = _PairAxes.from_buffer_copy(axes)
         elif n_axes > 1:
             raise ValueError("pair_axis: needed with several axes")
         n_pos = cos_sin.shape[0]

@@ -20,40 +20,65 @@ constexpr int kMaxWindow = 16;
 constexpr int kMaxRows = kMaxWindow + kSubblock - 1;
 constexpr int kHeads = 2;   // query heads of a half-warp whose rows are asked for together
 
-struct RowInfo {
+struct alignas(16) RowInfo {
   int b;        // request, -1: no request's row
   int at;       // position in the request's context
-  int first;    // the request's first new position
-  int end;      // one past its last
   int phys;     // physical page, -1: not appended, or not by this CTA
   int rot;      // positions within the table
+  int first;    // the request's first new position
+  int end;      // one past its last
 };
 
-// Where list row i belongs; `bad` gets the error bits.
-__device__ __forceinline__ RowInfo find_row(const AppendRopeParams& p, int i, int (&axis_pos)[4], uint32_t& bad) {
-  RowInfo r{-1, 0, 0, 0, -1, 0};
-  int lo = i, f = i, e = i + 1;
-  if (p.row_first) {   // the last request whose first row is not after row i
-    lo = 0;
-    int hi = p.B;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (p.row_first[mid] <= i) lo = mid;
-      else hi = mid;
+// Where list row i = base + lane belongs, for a whole warp; `bad` gets the error bits.  The requests' bounds and
+// lengths are read 32 at a time and passed between the lanes, so that few reads wait for one another (a search
+// by halves had log2 B of them in front of the CTA's first barrier).
+__device__ __forceinline__ RowInfo find_row(const AppendRopeParams& p, int base, int lane, int (&axis_pos)[4], uint32_t& bad) {
+  RowInfo r{-1, 0, -1, 0, 0, 0};
+  const int i = base + lane;
+  int b = i, f = i, e = i + 1, L;
+  if (p.row_first) {
+    int lo = 0;   // at most the request of row `base`, the last that begins there or before; it, with B > 31
+    for (int span = p.B > 31 ? p.B : 1; span > 1;) {
+      const int step = (span + 31) / 32, x = lane * step;
+      const unsigned m = __ballot_sync(0xffffffffu, x < span && p.row_first[lo + min(x, span - 1)] <= base);
+      const int k = m ? 31 - __clz(m) : 0;
+      lo += k * step;
+      span = min(step, span - k * step);
     }
-    f = p.row_first[lo];
-    e = p.row_first[lo + 1];
+    const int bound = p.row_first[min(lo + lane, p.B)], len = p.seq_len[min(lo + lane, p.B - 1)];
+    int k = 0;    // of the 32 from lo on, the last that begins at row i or before
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1)
+      if (__shfl_sync(0xffffffffu, bound, k + o) <= i && lo + k + o < p.B) k += o;
+    b = lo + k;
+    f = __shfl_sync(0xffffffffu, bound, k);
+    e = __shfl_sync(0xffffffffu, bound, min(k + 1, 31));
+    L = __shfl_sync(0xffffffffu, len, k);
+    if (k == 31) {   // it, or one of those behind
+      int hi = p.B;
+      while (hi - b > 1) {
+        const int mid = (b + hi) >> 1;
+        if (p.row_first[mid] <= i) b = mid;
+        else hi = mid;
+      }
+      f = p.row_first[b];
+      e = p.row_first[b + 1];
+      L = p.seq_len[b];
+    }
+    if (i >= p.n_rows || f > i || i >= e) return r;
+  } else {
+    if (lane >= p.window || i >= p.n_rows) return r;   // a row behind the window is of no request in it
+    L = p.seq_len[b];
   }
-  if (f > i || i >= e) return r;
-  const int64_t L = p.seq_len[lo], at = L - (int64_t(e) - i), first = L - (int64_t(e) - f);
+  const int64_t at = int64_t(L) - (int64_t(e) - i), first = int64_t(L) - (int64_t(e) - f);
   if (at < 0 || at / kPageTokens >= p.np_max || at > INT32_MAX - kPageTokens) {
     bad |= SPKV_DEVERR_PAGE_ID;
   } else {
-    r.b = lo;
+    r.b = b;
     r.at = static_cast<int>(at);
     r.first = static_cast<int>(max(first, int64_t(0)));
-    r.end = static_cast<int>(L);
-    const int ph = p.page_table[int64_t(lo) * p.np_max + at / kPageTokens];
+    r.end = L;
+    const int ph = p.page_table[int64_t(b) * p.np_max + at / kPageTokens];
     if (ph >= 0 && ph < p.n_phys) r.phys = ph;
     else bad |= SPKV_DEVERR_PHYS;
   }
@@ -114,8 +139,8 @@ __device__ __forceinline__ void store_pairs(uint16_t* row, int l, uint4 v) {
 // (which spill), 59 with CTAs of 512.
 template <bool Q4>
 __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_constant__ AppendRopeParams p) {
-  __shared__ RowInfo info[kMaxRows];
-  __shared__ int axis_pos[kMaxRows][4];
+  __shared__ RowInfo info[32];      // a warp looks up, the last is not of this window
+  __shared__ int axis_pos[32][4];
   __shared__ __align__(16) float rows[kMaxRows][kHeadDim];   // the cache's values of the new keys (4-bit: without g)
   pdl_wait();
   pdl_trigger();
@@ -139,17 +164,14 @@ __global__ void __launch_bounds__(256, 5) append_rope_kernel(const __grid_consta
       if (r < own && 2 * k + half < p.G) qv[k] = load_pairs(q + 2 * k * kHeadDim, l);
   };
   if (warp < own) ask(warp, true);
-  if (tid < kMaxRows) {
-    RowInfo ri{-1, 0, 0, 0, -1, 0};
-    if (tid < own + kSubblock - 1 && base + tid < p.n_rows) {
-      uint32_t bad = 0;
-      ri = find_row(p, base + tid, axis_pos[tid], bad);
-      if (tid < own && h == 0) flag_error(p.err, bad);
-      // its sub-block's first new row is one of the window's
-      const int opens = tid - min(ri.at % kSubblock, ri.at - ri.first);
-      if (opens < 0 || opens >= own) ri.b = ri.phys = -1;
-    }
-    info[tid] = ri;
+  if (warp == 0) {
+    uint32_t bad = 0;
+    RowInfo ri = find_row(p, base, lane, axis_pos[lane], bad);
+    if (lane < own && h == 0) flag_error(p.err, bad);
+    // its sub-block's first new row is one of the window's
+    const int opens = lane - min(ri.at % kSubblock, ri.at - ri.first);
+    if (opens < 0 || opens >= own) ri.b = ri.phys = -1;
+    info[lane] = ri;
   }
   __syncthreads();
 

@@ -386,6 +386,20 @@ def test_rows_in_front_count_as_held(q4):
 
 
 @pytest.mark.parametrize("q4", FORMATS)
+@pytest.mark.parametrize("B", [31, 32, 33, 70, 1100])
+def test_many_requests(q4, B):
+    """More requests than a warp looks through at once, most of them with a row or two or none."""
+    rng = np.random.default_rng(B)
+    lens = rng.choice([0, 0, 1, 1, 2, 19], B)
+    lens[B // 2: B // 2 + 40] = 0
+    lens[-1] = 3
+    b = Batch(q4, rng.integers(0, 40, B), lens, 2, 1, seed=B)
+    b.call(pair_axis=np.zeros(64, np.int64))
+    assert spkv.get_device_error(b.cache) == (0, 0)
+    b.check(b.expect())
+
+
+@pytest.mark.parametrize("q4", FORMATS)
 def test_rows_of_no_request(q4):
     """Rows before the first request, empty requests, and a call of nothing."""
     b = Batch(q4, [0, 9, 64], [5, 0, 4], 4, 2, seed=17, pad=6)
@@ -448,6 +462,8 @@ def test_refused_arguments():
     refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]))               # which axis turns which pair?
     refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[0] * 63)
     refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[2] * 64)
+    refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[-1] * 64)
+    refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=np.full(64, 2))
     assert refused(A, cos_sin=tab, pos=i32(np.zeros((2, 5))), pair_axis=[4] * 64).status == -1   # five axes
     assert refused(A, q=b.qd[:, :7].contiguous(), q_out=b.q_out[:, :7].contiguous(), cos_sin=tab).status == -1
     many = torch.zeros(2, 34, 128, dtype=torch.bfloat16, device=DEV)
