@@ -377,6 +377,11 @@ struct Cfg {
 
 constexpr int kCtaPages = 8;    // pages of a CTA, at least
 constexpr int kPartPages = 4;   // and of one that takes a part of a unit
+// Places between two units' pages where the pages are dealt: what a unit's end (the warps waiting for one another,
+// merges, the next queries) costs the CTA that meets it.  Without them such CTAs end 2 to 5 us after the others.
+// 0 / 4 / 6 / 8 places: 64 units of 129 pages 28.0 / 26.9 / 26.3 / 26.0 us, 61 of up to 129 (16 heads) 28.4 / 26.0 /
+// 26.3 / 26.9, 256 of 65 37.2 / 37.5 / 37.3 / 37.2, a step with 128 of 65 38.3 / 40.3 / 38.8 / 37.9.
+constexpr int kEndPages = 8;
 
 template <int CG, bool PACK>
 struct SmemQ4 {
@@ -406,15 +411,21 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
   if (ln == 0) p.lse[row] = L == 0.f ? -CUDART_INF_F : (M + log2f(L)) * kLn2;
 }
 
-// The pages of all units form one sequence of T pages, dealt evenly to N CTAs, three to an SM so that one's
-// look-ups and merges overlap the others' pages.  A CTA's segments are the units that it meets.  All
-// threads look up its pages (128 at a time), each page-head arrives with one bulk copy, whoever is through
-// with a stage copies its next page there, and at a segment's end the warps' states are merged in shared
-// memory: into the output, or into the workspace for a unit that spans CTAs (a CTA has at most two such:
-// its first and its last).  The CTA that arrives last at such a unit merges its parts in order, so the
-// result does not depend on which one that is; every CTA arrives, so the counters are zero again after
-// the call.  BY_UNIT (few units, short lists): CTA c takes part c % parts of unit c / parts, which spares it
-// the search for its pages.
+// The pages of all units form one sequence of T pages, dealt evenly (with kEndPages places between units) to N
+// CTAs, three to an SM so that one's look-ups and merges overlap the others' pages.  A CTA's segments are the
+// units that it meets.  All threads look up its pages (128 at a time), each page-head arrives with one bulk
+// copy, whoever is through with a stage copies its next page there, and at a segment's end the warps' states
+// are merged in shared memory: into the output, or into the workspace for a unit that spans CTAs (a CTA has
+// at most two such: its first and its last).  The CTA that arrives last at such a unit merges its parts in
+// order, so the result does not depend on which one that is; every CTA arrives, so the counters are zero again
+// after the call.  BY_UNIT (few units, short lists): CTA c takes part c % parts of unit c / parts, which spares
+// it the search for its pages.
+//
+// Measured (GB300): 256 units of 65 pages, 4 heads 37 us = 153 MB at 4.1 TB/s (0.61 of the copy rate); 64 units of
+// 129 pages, 5 heads 26 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
+// the first pages are there (lengths, lists, page table and page read one after the other), 25 us at 6.3 TB/s, and
+// 4 us from the first CTA's end to the last's, merges included.  The other two are bound by instructions (1165 a
+// page and warp for up to 4 heads, 1411 for 8: half unpack and scale codes) and by the same ends.
 template <int CG, bool PACK, bool BY_UNIT>
 __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasPerSm)
     attn_q4_kernel(const __grid_constant__ AttnQ4Params p4) {
@@ -478,10 +489,12 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     __syncthreads();
     return before + x - own;
   };
-  // ---- this CTA's pages [x0, x1) of T; the window of units for the look-ups, and its first page
+  // ---- this CTA's pages [x0, x1) of T, x1 as far as the window of units goes that it looks up; that window's first
+  // unit and page.  Page x, of unit u, is place x + kEndPages u of those that are dealt.
   int x0, x1, base_u = 0, base_x = 0;
+  bool last = true;           // x1 is the CTA's end
   int unit_parts = 1;
-  int share = 1, extra = 0;   // pages of a CTA, and how many CTAs take one more
+  int share = 1, extra = 0;   // places of a CTA, and how many CTAs take one more
   auto cta_begin = [&](int c) { return c * share + min(c, extra); };
   auto cta_of = [&](int x) {
     const int big = extra * (share + 1);
@@ -497,6 +510,19 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     if (tid == 0) S.first[C::kWindow] = base_x + total;
     __syncthreads();
     return base_x + total;
+  };
+  // the first page at place v of the window or behind it
+  auto page_at = [&](int v) {
+    int m = 0;
+#pragma unroll
+    for (int o = C::kWindow / 2; o > 0; o >>= 1)
+      if (S.first[m + o] + kEndPages * (base_u + m + o) <= v) m += o;
+    return min(v - kEndPages * (base_u + m), S.first[m + 1]);
+  };
+  auto bound = [&]() {
+    const int v = cta_begin(cta + 1);
+    last = base_u + C::kWindow >= U || v < S.first[C::kWindow] + kEndPages * (base_u + C::kWindow);
+    x1 = last ? page_at(v) : S.first[C::kWindow];
   };
   if (BY_UNIT) {
     base_u = cta / p4.parts;
@@ -524,24 +550,25 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       if (count(u) == 0) write_empty(u);
     const int N = min(T, static_cast<int>(gridDim.x));
     if (cta >= N) return;
-    share = T / N;
-    extra = T - share * N;
-    x0 = cta_begin(cta);
-    x1 = cta_begin(cta + 1);
+    const int V = T + kEndPages * U;
+    share = V / N;
+    extra = V - share * N;
     if (U > C::kWindow) {
-      int t = 0;   // the last thread whose units begin at or before x0
+      const int k = (U + C::kThreads - 1) / C::kThreads, v = cta_begin(cta);
+      int t = 0;   // the last thread whose units begin at or before v
 #pragma unroll
       for (int o = C::kThreads / 2; o > 0; o >>= 1)
-        if (S.scan[t + o] <= x0) t += o;
-      base_u = t * ((U + C::kThreads - 1) / C::kThreads);
+        if (S.scan[t + o] + kEndPages * min((t + o) * k, U) <= v) t += o;
+      base_u = t * k;
       base_x = S.scan[t];
       look();
     }
+    x0 = page_at(cta_begin(cta));
+    bound();
   }
 
   Warp4<PACK> w;
   int cur = -1;        // the unit that the warps' states are of
-  bool head = true;    // whether it is the CTA's first
   bool ok = true;
   auto take = [&](int u) {   // the warps' states become those of unit u
     const int64_t row = row_of(u);
@@ -553,10 +580,9 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     w.reset();
     cur = u;
   };
-  for (int x = x0; x < x1;) {
+  for (int x = x0; x < x1 || !last;) {
     // ---- as many pages as there are descriptors, and as the window has
-    const int end = min(x1, S.first[C::kWindow]);   // of the pages in the window
-    const int cnt = min(C::kDesc, end - x);         // none if the window's units are all empty
+    const int cnt = min(C::kDesc, x1 - x);          // none if the window's units are all empty
     int mine = 0;                                   // unit of page x + tid: the last that starts there or before
 #pragma unroll
     for (int o = C::kWindow / 2; o > 0; o >>= 1)
@@ -590,10 +616,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       // ---- a segment: descriptors [kb, ke)
       const int su = S.desc[kb].y >> 8, u = base_u + su;
       const int f = S.first[su], e = S.first[su + 1], ke = min(cnt, e - x);
-      if (u != cur) {
-        take(u);
-        head = false;
-      }
+      if (u != cur) take(u);
       for (int i = kb + (team + TEAMS - (j0 + kb) % TEAMS) % TEAMS; i < ke && ok; i += TEAMS) {
         const int j = j0 + i, s = j % NS;
         ok = __all_sync(0xffffffffu, mbar_wait(&S.full[j % L], (j / L) & 1, p.wait_ns));
@@ -617,7 +640,8 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       // ---- its end: the teams' states merged, a warp taking a query head at a time
       w.store(S.state[team], c8, lane);
       w.reset();   // nothing of it is kept over the merges
-      const bool whole = f >= x0 && e <= x1;
+      const int gap = kEndPages * u;
+      const bool whole = f >= x0 && e <= x1;   // a unit is in the window or out of it
       __syncthreads();
       const int64_t row = S.row;
       const float gv = S.gv;
@@ -638,7 +662,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
         if (whole) {
           write_row(p, row + g, lane, M, sum, acc, gv);
         } else {
-          const int64_t at = (BY_UNIT ? cta : 2 * cta + (head ? 0 : 1)) * 16 + g;
+          const int64_t at = (BY_UNIT ? cta : 2 * cta + (f + gap > cta_begin(cta) ? 1 : 0)) * 16 + g;
           *reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 4 * lane) = acc;
           if (lane == 0) {
             p.ws_m[at] = M;
@@ -649,9 +673,9 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       __syncthreads();   // the states are free again; this CTA's part is written
       if (whole) continue;
       // ---- a unit of several CTAs: the last to arrive merges
-      const int c0 = BY_UNIT ? cta - cta % p4.parts : cta_of(f);
-      const int parts = BY_UNIT ? unit_parts : cta_of(e - 1) - c0 + 1;
-      const int late = !BY_UNIT && f > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
+      const int c0 = BY_UNIT ? cta - cta % p4.parts : cta_of(f + gap);
+      const int parts = BY_UNIT ? unit_parts : cta_of(e - 1 + gap) - c0 + 1;
+      const int late = !BY_UNIT && f + gap > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
       if (tid == 0) {
         int before;   // release: this CTA's part, which the barrier has ordered before; acquire: the others'
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.ws_parts + u) : "memory");
@@ -718,7 +742,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     }
     if (__syncthreads_or(!ok)) ok = false;   // the descriptors and the window are free again
     x += cnt;
-    if (x >= x1) break;
+    if (x >= x1 && last) break;
     // the next window begins with the unit of the next page, or behind this one
     int next = C::kWindow;
     if (x < S.first[C::kWindow]) {
@@ -730,7 +754,10 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     base_x = S.first[next];
     base_u += next;
     __syncthreads();
-    if (!BY_UNIT) look();   // one unit's window stays
+    if (!BY_UNIT) {   // one unit's window stays
+      look();
+      bound();
+    }
   }
   // no copy is left in flight (with the full limit: copies end in microseconds)
   if (tid < NS && S.copied[tid] >= 0) mbar_wait(&S.full[S.copied[tid] % L], (S.copied[tid] / L) & 1);

@@ -145,6 +145,26 @@ def test_attention_long_lists(Hq, Hk, B, pages):
             assert abs(lse[b, g] - wl) <= dx * (1 + abs(wl))
 
 
+@pytest.mark.parametrize("B,Hk,G,most", [(100, 3, 2, 7), (257, 1, 9, 3), (512, 8, 1, 2), (300, 2, 4, 12)])
+@pytest.mark.parametrize("empty", [0.0, 0.5, 0.99])
+def test_attention_many_units(B, Hk, G, most, empty):
+    """More units than are looked up at a time, most of them short or empty, and two long ones."""
+    rng = np.random.default_rng(B + most)
+    c = Cache(Hk, 2, 40, [2560, 2500], seed=B)
+    c.handle = spkv.paged_kv_create_q4(c.pool, c.gk_d, c.gv_d, c.ksum, c.cnt_d, max_units=B * Hk)
+    full = c.pt[0][:39]      # pages of 64 tokens; requests share them
+    c.B, c.np_max, c.L = B, 39, np.full(B, 39 * 64, np.int32)
+    c.pt = np.stack([rng.permutation(full) for _ in range(B)]).astype(np.int32)
+    n = rng.integers(1, most + 1, (B, Hk)).astype(np.int32)
+    n[rng.random((B, Hk)) < empty] = 0
+    n[B // 3, 0], n[B - 2, Hk - 1] = 39, 31
+    sel = np.tile(np.arange(39, dtype=np.int32), (B, Hk, 1))
+    x, q = queries(B, G * Hk, seed=B)
+    out, lse = c.attend(q, sel, n)
+    assert spkv.get_device_error(c.handle) == (0, 0)
+    check(out, lse, ref.attention(x, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
+
+
 @pytest.mark.parametrize("q_scale,key_scale", [(1e-6, 1.0), (30.0, 1.0), (1e4, 1e-3), (1.0, 0.0)])
 def test_attention_score_ranges(q_scale, key_scale):
     """Flat and peaked weights, queries outside f16's range, keys of zeros: the running maximum rises."""
