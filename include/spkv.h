@@ -169,7 +169,9 @@ typedef struct {
 /* paged_kv_create for a 4-bit cache.  On the handle work paged_kv_append_rope, paged_kv_unpack_q4,
  * score_blocks(_dir), select_topk, resident_setdiff, lru_bucket_update, select_resident_update and
  * sparse_decode_attn, _slots, _dir, with the arguments they have for a bf16 handle; the other calls,
- * which read or write bf16 pages, return SPKV_EUNSUPPORTED (paged_kv_unpack_q4 gives them such pages). */
+ * which read or write bf16 pages, return SPKV_EUNSUPPORTED (paged_kv_unpack_q4 gives them such pages).
+ * The handle is used where the device is current that was so at its creation, and the attention takes
+ * B * n_kv_heads * (sel_stride + 8) < 2^31 (else SPKV_EINVAL). */
 int paged_kv_create_q4(const spkv_desc_q4* desc, void* stream, spkv_cache_t* out);
 
 /* Rotary positions of paged_kv_append_rope.
@@ -195,7 +197,8 @@ typedef struct {
  *   (x_j, x_{j+64}) -> (x_j c - x_{j+64} s, x_{j+64} c + x_j s)
  * by the cos c and sin s of its position; the queries are rounded to bf16 into q_out, the keys (rounded
  * to bf16, or from fp32 to the 4-bit format) and the values go to the cache, page_cnt is raised and
- * the sub-block sums that changed are formed again in paged_kv_append's order.
+ * the sub-block sums that changed are formed again in paged_kv_append's order (rows in front of the
+ * new ones count as held, rows behind them as far as page_cnt says).
  *   k_new, v_new : device bf16, rows k_stride (v_stride) elements apart, each [n_kv_heads][128]
  *   q            : device bf16, rows q_stride apart, each [Hq][128], or NULL (no queries)
  *   q_out        : device bf16 [n_rows][Hq][128]; may be q itself where q is contiguous
