@@ -11,6 +11,8 @@
 // f16's range (its bf16 has 8 bits); the weights are split into f16 hi + lo parts (22 bits).
 #include <math_constants.h>
 
+#include <cmath>
+
 #include "q4.cuh"
 
 namespace spkv {
@@ -375,8 +377,9 @@ struct Cfg {
   static_assert(L % NS == 0 && L % TEAMS == 0, "barriers");
 };
 
-constexpr int kCtaPages = 8;    // pages of a CTA, at least
-constexpr int kPartPages = 4;   // and of one that takes a part of a unit
+// Pages of a CTA where they are dealt, at least (few units have so few: 4 spares 32 units of 9 pages 4 us, costs one of
+// 500 pages 5), of a part of a unit, at least, and of a part, at most, where the launch alone lets CTAs take units.
+constexpr int kCtaPages = 8, kPartPages = 4, kUnitPages = 16;
 // Places between two units' pages where the pages are dealt: what a unit's end (the warps waiting for one another,
 // merges, the next queries) costs the CTA that meets it.  Without them such CTAs end 2 to 5 us after the others.
 // 0 / 4 / 6 / 8 places: 64 units of 129 pages 28.0 / 26.9 / 26.3 / 26.0 us, 61 of up to 129 (16 heads) 28.4 / 26.0 /
@@ -418,11 +421,12 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
 // are merged in shared memory: into the output, or into the workspace for a unit that spans CTAs (a CTA has
 // at most two such: its first and its last).  The CTA that arrives last at such a unit merges its parts in
 // order, so the result does not depend on which one that is; every CTA arrives, so the counters are zero again
-// after the call.  BY_UNIT (few units, short lists): CTA c takes part c % parts of unit c / parts, which spares
-// it the search for its pages.
+// after the call.  by_unit (units that fill the CTAs, of about one length): CTA c takes part c % parts of unit
+// c / parts and meets no unit's end but its own; with BY_UNIT (short parts) it need not count the others' pages
+// either.
 //
 // Measured (GB300): 256 units of 65 pages, 4 heads 37 us = 153 MB at 4.1 TB/s (0.61 of the copy rate); 64 units of
-// 129 pages, 5 heads 26 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
+// 129 pages, 5 heads 25 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
 // the first pages are there (lengths, lists, page table and page read one after the other), 25 us at 6.3 TB/s, and
 // 4 us from the first CTA's end to the last's, merges included.  The other two are bound by instructions (1165 a
 // page and warp for up to 4 heads, 1411 for 8: half unpack and scale codes) and by the same ends.
@@ -493,6 +497,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   // unit and page.  Page x, of unit u, is place x + kEndPages u of those that are dealt.
   int x0, x1, base_u = 0, base_x = 0;
   bool last = true;           // x1 is the CTA's end
+  bool by_unit = BY_UNIT;     // the CTA has a part of one unit
   int unit_parts = 1;
   int share = 1, extra = 0;   // places of a CTA, and how many CTAs take one more
   auto cta_begin = [&](int c) { return c * share + min(c, extra); };
@@ -527,10 +532,10 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   if (BY_UNIT) {
     base_u = cta / p4.parts;
     const int n = count(base_u), part = cta % p4.parts;
-    unit_parts = min(p4.parts, (n + kPartPages - 1) / kPartPages);
+    unit_parts = min(p4.parts, (n + p4.part_pages - 1) / p4.part_pages);
     if (part == 0 && n == 0) write_empty(base_u);
     if (part >= unit_parts) return;
-    x0 = n * part / unit_parts;   // (3 SMs CTAs of 4 pages at most: no overflow)
+    x0 = n * part / unit_parts;   // (a CTA has at most 2 kUnitPages: no overflow)
     x1 = n * (part + 1) / unit_parts;
     if (tid == 0) S.first[0] = 0;
     for (int i = tid; i < C::kWindow; i += C::kThreads) S.first[i + 1] = n;
@@ -548,8 +553,9 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     }
     for (int u = cta; u < U; u += gridDim.x)
       if (count(u) == 0) write_empty(u);
+    by_unit = p4.parts > 0 && int64_t(T) * 8 >= int64_t(U) * p.sel_stride * 7;
     const int N = min(T, static_cast<int>(gridDim.x));
-    if (cta >= N) return;
+    if (cta >= (by_unit ? U * p4.parts : N)) return;
     const int V = T + kEndPages * U;
     share = V / N;
     extra = V - share * N;
@@ -563,8 +569,16 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       base_x = S.scan[t];
       look();
     }
-    x0 = page_at(cta_begin(cta));
-    bound();
+    if (by_unit) {
+      const int f = S.first[cta / p4.parts], n = S.first[cta / p4.parts + 1] - f, part = cta % p4.parts;
+      unit_parts = min(p4.parts, (n + p4.part_pages - 1) / p4.part_pages);
+      if (part >= unit_parts) return;
+      x0 = f + static_cast<int>(int64_t(n) * part / unit_parts);
+      x1 = f + static_cast<int>(int64_t(n) * (part + 1) / unit_parts);
+    } else {
+      x0 = page_at(cta_begin(cta));
+      bound();
+    }
   }
 
   Warp4<PACK> w;
@@ -662,7 +676,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
         if (whole) {
           write_row(p, row + g, lane, M, sum, acc, gv);
         } else {
-          const int64_t at = (BY_UNIT ? cta : 2 * cta + (f + gap > cta_begin(cta) ? 1 : 0)) * 16 + g;
+          const int64_t at = (2 * cta + (!by_unit && f + gap > cta_begin(cta) ? 1 : 0)) * 16 + g;
           *reinterpret_cast<float4*>(p.ws_o + at * kHeadDim + 4 * lane) = acc;
           if (lane == 0) {
             p.ws_m[at] = M;
@@ -673,9 +687,9 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
       __syncthreads();   // the states are free again; this CTA's part is written
       if (whole) continue;
       // ---- a unit of several CTAs: the last to arrive merges
-      const int c0 = BY_UNIT ? cta - cta % p4.parts : cta_of(f + gap);
-      const int parts = BY_UNIT ? unit_parts : cta_of(e - 1 + gap) - c0 + 1;
-      const int late = !BY_UNIT && f + gap > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
+      const int c0 = by_unit ? cta - cta % p4.parts : cta_of(f + gap);
+      const int parts = by_unit ? unit_parts : cta_of(e - 1 + gap) - c0 + 1;
+      const int late = !by_unit && f + gap > cta_begin(c0) ? 1 : 0;   // not the first unit of c0
       if (tid == 0) {
         int before;   // release: this CTA's part, which the barrier has ordered before; acquire: the others'
         asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.ws_parts + u) : "memory");
@@ -693,7 +707,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
         for (int k = 0; k < HG; ++k) M[k] = -CUDART_INF_F, sum[k] = 0.f, acc[k] = make_float4(0.f, 0.f, 0.f, 0.f);
         auto place = [&](int i, int k) {   // the unit is its CTA's first, but perhaps where it begins
           const int c = c0 + i;
-          return int64_t(BY_UNIT ? c : 2 * c + (i == 0 ? late : 0)) * 16 + warp + C::W * k;
+          return int64_t(2 * c + (i == 0 ? late : 0)) * 16 + warp + C::W * k;
         };
         for (int i0 = 0; i0 < parts; i0 += kBatch) {
           float m[HG], l[HG];
@@ -756,7 +770,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     __syncthreads();
     if (!BY_UNIT) {   // one unit's window stays
       look();
-      bound();
+      if (!by_unit) bound();
     }
   }
   // no copy is left in flight (with the full limit: copies end in microseconds)
@@ -769,9 +783,18 @@ cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
   const int64_t U = int64_t(p.a.B) * p.a.Hk, slots = int64_t(C::kCtasPerSm) * c->sm_count;
   const dim3 block(C::kThreads);
   const size_t smem = sizeof(SmemQ4<CG, PACK>);
-  p.parts = (p.a.sel_stride + kPartPages - 1) / kPartPages;
-  if (U * p.parts <= slots)
+  // CTAs take parts of units (us; dealt / by unit): 2 units of 17 pages 10.3 / 6.8, 64 of 33 13.9 / 10.4, 128 of 17 14.5 /
+  // 11.1, 256 of 5 13.4 / 8.3, 400 of 17 24.5 / 18.5.  Not where parts are long, as lists may then be of very different
+  // lengths: 61 of 0 to 129 27 / 33; but there the kernel, which counts them, does where they are not: 64 of 129 26.1 / 25.3.
+  // A part's pages: the CTAs' time grows with them and the merge's with the parts, so with the root of the length
+  // (129 pages in 16, 26, 33 parts 9.8, 10.2, 10.5; 500 in 16, 32, 63: 18.0, 15.3, 15.6).
+  const int n = p.a.sel_stride;
+  p.part_pages = max(kPartPages, static_cast<int>(0.6 * std::sqrt(static_cast<double>(n))));
+  p.parts = static_cast<int>(min(int64_t(n + p.part_pages - 1) / p.part_pages, max(slots / U, int64_t(1))));
+  const int64_t most = int64_t(kUnitPages) * p.parts * (U > C::kWindow ? 2 : 1);   // finding one's pages among more is slow
+  if (U <= slots && n <= most)
     return launch_pdl(attn_q4_kernel<CG, PACK, true>, dim3(static_cast<unsigned>(U * p.parts)), block, smem, st, p);
+  if (U > C::kWindow || U * p.parts * 5 < slots * 4) p.parts = 0;   // a fifth of the CTAs would have nothing
   const int64_t want = (U * p.a.sel_stride + kCtaPages - 1) / kCtaPages;
   return launch_pdl(attn_q4_kernel<CG, PACK, false>, dim3(static_cast<unsigned>(min(want, slots))), block, smem, st, p);
 }
@@ -795,7 +818,7 @@ cudaError_t attn_q4_init_attributes() {
 }
 
 cudaError_t launch_attn_q4(const spkv_cache* c, const AttnParams& a, cudaStream_t st) {
-  const AttnQ4Params p{a, c->pool4, c->k_scale, c->v_scale, 1};
+  const AttnQ4Params p{a, c->pool4, c->k_scale, c->v_scale, 1, 1};
   if (a.G <= 4) return launch_one<1, true>(c, p, st);
   if (a.G <= 8) return launch_one<1, false>(c, p, st);
   return launch_one<2, false>(c, p, st);

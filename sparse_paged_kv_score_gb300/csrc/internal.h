@@ -166,7 +166,7 @@ struct AttnQ4Params {
   const uint8_t* pool;
   const float* k_scale;
   const float* v_scale;
-  int parts;                     // CTAs of a unit, where each takes a part of one
+  int parts, part_pages;  // CTAs a unit where CTAs take units, at most; pages of a part, at least
 };
 
 // Parameters of the rotating append (either cache format).

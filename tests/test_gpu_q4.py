@@ -165,6 +165,46 @@ def test_attention_many_units(B, Hk, G, most, empty):
     check(out, lse, ref.attention(x, c.blob, c.gk, c.gv, c.pt, sel, n, c.L))
 
 
+@pytest.mark.parametrize("B,Hk,G,pages", [(1, 1, 4, 2000), (61, 1, 9, 129), (40, 2, 5, 300), (200, 1, 2, 40), (3, 1, 1, 20000),
+                                           (64, 2, 16, 70), (128, 2, 1, 9), (300, 1, 4, 17)])
+@pytest.mark.parametrize("short", [0, 1, 2])
+def test_attention_dealing(B, Hk, G, pages, short):
+    """Lists of one length, lists a little shorter (dealt by unit as well), and lists of every length, over few physical
+    pages: for each list the mean of its pages' weighted values."""
+    rng = np.random.default_rng(pages + short)
+    c = Cache(Hk, 1, 12, [768], seed=B)
+    h = spkv.paged_kv_create_q4(c.pool, c.gk_d, c.gv_d, None, None, max_units=B * Hk)
+    which = rng.integers(0, 12, (B, pages))
+    pt = c.pt[0][which].astype(np.int32)
+    n = np.full((B, Hk), pages, np.int32)
+    if short:
+        n -= rng.integers(0, (pages // 20 if short == 1 else pages) + 1, (B, Hk)).astype(np.int32)
+    sel = np.tile(np.arange(pages, dtype=np.int32), (B, Hk, 1))
+    x, q = queries(B, G * Hk, seed=pages)
+    out, lse = torch.zeros(B, G * Hk, 128, device=DEV), torch.zeros(B, G * Hk, device=DEV)
+    for _ in range(2):     # the second call finds the workspace as the first left it
+        spkv.sparse_decode_attn(h, q, i32(pt), i32(sel), i32(n), i32(np.full(B, 64 * pages)), out.fill_(7), lse.fill_(7))
+        assert spkv.get_device_error(h) == (0, 0)
+        o, l = out.cpu().numpy().astype(np.float64), lse.cpu().numpy().astype(np.float64)
+        for kv in range(Hk):
+            k = ref.rows(c.blob[kv, c.pt[0]], True).reshape(-1, 128) * float(c.gk[kv])
+            v = ref.rows(c.blob[kv, c.pt[0]], False).reshape(12, 64, 128) * float(c.gv[kv])
+            for g in range(kv * G, kv * G + G):
+                y = x[:, g].astype(np.float64) @ k.T / np.sqrt(128)       # [B][12 * 64]
+                dx = 136 * 2.0 ** -23 * (np.abs(x[:, g].astype(np.float64)) @ np.abs(k).T).max() / np.sqrt(128)
+                m = y.max(1)
+                w = np.exp(y - m[:, None]).reshape(B, 12, 64)
+                num, den = np.einsum("bpt,ptd->bpd", w, v), w.sum(2)
+                for b in range(B):
+                    times = np.bincount(which[b, :n[b, kv]], minlength=12)
+                    if n[b, kv] == 0:
+                        assert np.all(o[b, g] == 0) and np.isneginf(l[b, g])
+                        continue
+                    s = times @ den[b]
+                    assert np.abs(o[b, g] - times @ num[b] / s).max() <= 2 * (dx + 2.0 ** -19) * np.abs(v).max()
+                    assert abs(l[b, g] - m[b] - np.log(s)) <= dx + 2.0 ** -19 * (1 + abs(l[b, g]))
+
+
 @pytest.mark.parametrize("q_scale,key_scale", [(1e-6, 1.0), (30.0, 1.0), (1e4, 1e-3), (1.0, 0.0)])
 def test_attention_score_ranges(q_scale, key_scale):
     """Flat and peaked weights, queries outside f16's range, keys of zeros: the running maximum rises."""
