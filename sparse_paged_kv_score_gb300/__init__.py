@@ -240,7 +240,7 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
     vp, vs = _rows(v_new, "v_new", n, Hk, dev)
     rope, axes, qp, qs, Hq, qo = None, None, None, 0, 0, None
     if cos_sin is not None:
-        n_axes = 1 if pos is None or pos.dim() == 1 else pos.shape[1]
+        n_axes = 1 if pos is None or pos.dim() < 2 else pos.shape[1]
         if pair_axis is not None:
             axes = bytes(pair_axis if isinstance(pair_axis, (list, tuple)) else [int(a) for a in pair_axis])
             if len(axes) != HEAD_DIM // 2 or max(axes) >= n_axes:

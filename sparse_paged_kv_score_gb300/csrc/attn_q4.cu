@@ -340,7 +340,7 @@ __device__ __forceinline__ int page_of(const AttnParams& p, int u, int b, int i,
   const int lp = p.sel[int64_t(u) * p.sel_stride + i];
   uint32_t bad = 0;
   int valid = 0, ph = 0;
-  if (lp < 0 || lp >= p.np_max) {
+  if (lp < 0 || lp >= p.np_max || lp >= (1 << 25)) {   // 64 lp stays within int
     bad = SPKV_DEVERR_PAGE_ID;
   } else {
     const int v = min(kPageTokens, p.seq_len[b] - kPageTokens * lp);

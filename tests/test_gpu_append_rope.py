@@ -459,6 +459,8 @@ def test_refused_arguments():
     refused(E, q=b.qd, q_out=b.q_out)                                # queries are rotated or not given
     refused(E, q=b.qd, cos_sin=tab)                                  # nowhere to write them
     refused(E, pos=i32([1, 2]))
+    refused(E, cos_sin=tab, pos=i32(1))
+    refused(E, cos_sin=tab, pos=i32([[[1], [2]]]), pair_axis=[0] * 64)
     refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]))               # which axis turns which pair?
     refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[0] * 63)
     refused(E, cos_sin=tab, pos=i32([[1, 2], [3, 4]]), pair_axis=[2] * 64)

@@ -264,6 +264,18 @@ def test_attention_bad_entries_are_skipped():
     check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, good, gn, c.L))
 
 
+def test_attention_page_ids_past_the_positions():
+    """Page ids whose tokens would lie past 2^31 are bad entries, though the table goes on."""
+    c = Cache(1, 1, 1, [64], seed=23)
+    x, q = queries(1, 4)
+    wide = torch.zeros(1, (1 << 25) + 8, dtype=torch.int32, device=DEV)
+    out, lse = torch.zeros(1, 4, 128, device=DEV), torch.zeros(1, 4, device=DEV)
+    spkv.sparse_decode_attn(c.handle, q, wide, i32([[[0, 1 << 25, (1 << 25) + 1]]]), i32([[3]]), i32([64]), out, lse)
+    assert spkv.get_device_error(c.handle)[1] == spkv.DEVERR["PAGE_ID"]
+    c.pt[:] = 0
+    check(out, lse, ref.attention(x, c.blob, c.gk, c.gv, c.pt, np.zeros((1, 1, 1), int), np.array([[1]]), c.L))
+
+
 def test_attention_runs_of_bad_entries():
     """Runs of bad entries longer than any ring of stages, between good ones."""
     c = Cache(1, 2, 8, [512, 450], seed=22)
@@ -428,6 +440,11 @@ def test_refused_calls():
         spkv.paged_kv_unpack_q4(bfc, one, torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV),
                                 torch.zeros(1, 1, 64, 128, dtype=torch.bfloat16, device=DEV))
     assert e.value.status == U
+    # an output whose rows begin between two pairs of values
+    odd = torch.zeros(8 * 128 + 1, device=DEV)[1:].view(1, 8, 128)
+    with pytest.raises(spkv.SpkvError) as e:
+        spkv.sparse_decode_attn(c.handle, q, i32(c.pt), i32(np.zeros((1, 2, 1))), i32([[1, 1]]), i32(c.L), odd, lse)
+    assert e.value.status == -1
     assert spkv.get_device_error(c.handle) == (0, 0)
 
 
