@@ -105,8 +105,9 @@ void fill_common(AttnParams& p, spkv_cache_t c, const void* q, int B, int Hq, fl
 // The selected-pages attention in the handle's format; grid bounds the persistent bf16 kernel's CTAs.
 int launch_sparse(spkv_cache_t c, const AttnParams& p, int grid, void* stream) {
   if (c->pool4) {
-    // it numbers all units' pages, and a few places for each unit, in 32 bits, and writes two values of a row together
-    if (!on_device(c) || !aligned(p.out, 8) || int64_t(p.B) * p.Hk * (int64_t(p.sel_stride) + 8) >= (int64_t(1) << 31)) return SPKV_EINVAL;
+    // it numbers tokens, and all units' pages and a few places for each unit, in 32 bits, and writes two values of a
+    // row together
+    if (!on_device(c) || !aligned(p.out, 8) || p.np_max > (1 << 25) || int64_t(p.B) * p.Hk * (int64_t(p.sel_stride) + 8) >= (int64_t(1) << 31)) return SPKV_EINVAL;
     return status_of(spkv::launch_attn_q4(c, p, as_stream(stream)));
   }
   return status_of(spkv::launch_attn(c, p, false, grid, as_stream(stream)));

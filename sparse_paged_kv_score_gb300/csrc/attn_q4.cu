@@ -340,7 +340,7 @@ __device__ __forceinline__ int page_of(const AttnParams& p, int u, int b, int i,
   const int lp = p.sel[int64_t(u) * p.sel_stride + i];
   uint32_t bad = 0;
   int valid = 0, ph = 0;
-  if (lp < 0 || lp >= p.np_max || lp >= (1 << 25)) {   // 64 lp stays within int
+  if (lp < 0 || lp >= p.np_max) {
     bad = SPKV_DEVERR_PAGE_ID;
   } else {
     const int v = min(kPageTokens, p.seq_len[b] - kPageTokens * lp);
@@ -422,15 +422,18 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
 // at most two such: its first and its last).  The CTA that arrives last at such a unit merges its parts in
 // order, so the result does not depend on which one that is; every CTA arrives, so the counters are zero again
 // after the call.  by_unit (units that fill the CTAs, of about one length): CTA c takes part c % parts of unit
-// c / parts and meets no unit's end but its own; with BY_UNIT (short parts) it need not count the others' pages
-// either.
+// c / parts and meets no unit's end but its own.  MODE: pages dealt (kDealt), so or by unit as the pages turn out
+// (kEither), or by unit without counting other units' pages (kByUnit).  (With kEither alone for the first two 256
+// units of 65 pages take 0.5 us more.)
 //
 // Measured (GB300): 256 units of 65 pages, 4 heads 37 us = 153 MB at 4.1 TB/s (0.61 of the copy rate); 64 units of
 // 129 pages, 5 heads 25 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
 // the first pages are there (lengths, lists, page table and page read one after the other), 25 us at 6.3 TB/s, and
 // 4 us from the first CTA's end to the last's, merges included.  The other two are bound by instructions (1165 a
 // page and warp for up to 4 heads, 1411 for 8: half unpack and scale codes) and by the same ends.
-template <int CG, bool PACK, bool BY_UNIT>
+enum Mode { kDealt, kEither, kByUnit };
+
+template <int CG, bool PACK, Mode MODE>
 __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasPerSm)
     attn_q4_kernel(const __grid_constant__ AttnQ4Params p4) {
   using C = Cfg<CG, PACK>;
@@ -454,7 +457,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     // assumed; a prefetch reads nothing).
     const int64_t x = int64_t(U) * p.sel_stride * cta / gridDim.x, at = x + 32 * tid;
     const int u = static_cast<int>(x / p.sel_stride);
-    if (cta == 0 || BY_UNIT)
+    if (cta == 0 || MODE == kByUnit)
       for (int i = 32 * tid; i < U; i += 32 * C::kThreads) prefetch_l2(p.n_sel + i);
     if (tid < 4 && at < int64_t(U) * p.sel_stride) {
       prefetch_l2(p.sel + at);
@@ -497,7 +500,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
   // unit and page.  Page x, of unit u, is place x + kEndPages u of those that are dealt.
   int x0, x1, base_u = 0, base_x = 0;
   bool last = true;           // x1 is the CTA's end
-  bool by_unit = BY_UNIT;     // the CTA has a part of one unit
+  bool by_unit = MODE == kByUnit;   // the CTA has a part of one unit
   int unit_parts = 1;
   int share = 1, extra = 0;   // places of a CTA, and how many CTAs take one more
   auto cta_begin = [&](int c) { return c * share + min(c, extra); };
@@ -529,7 +532,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     last = base_u + C::kWindow >= U || v < S.first[C::kWindow] + kEndPages * (base_u + C::kWindow);
     x1 = last ? page_at(v) : S.first[C::kWindow];
   };
-  if (BY_UNIT) {
+  if (MODE == kByUnit) {
     base_u = cta / p4.parts;
     const int n = count(base_u), part = cta % p4.parts;
     unit_parts = min(p4.parts, (n + p4.part_pages - 1) / p4.part_pages);
@@ -553,7 +556,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     }
     for (int u = cta; u < U; u += gridDim.x)
       if (count(u) == 0) write_empty(u);
-    by_unit = p4.parts > 0 && int64_t(T) * 8 >= int64_t(U) * p.sel_stride * 7;
+    by_unit = MODE == kEither && int64_t(T) * 8 >= int64_t(U) * p.sel_stride * 7;
     const int N = min(T, static_cast<int>(gridDim.x));
     if (cta >= (by_unit ? U * p4.parts : N)) return;
     const int V = T + kEndPages * U;
@@ -768,7 +771,7 @@ __global__ void __launch_bounds__(Cfg<CG, PACK>::kThreads, Cfg<CG, PACK>::kCtasP
     base_x = S.first[next];
     base_u += next;
     __syncthreads();
-    if (!BY_UNIT) {   // one unit's window stays
+    if (MODE != kByUnit) {   // one unit's window stays
       look();
       if (!by_unit) bound();
     }
@@ -785,7 +788,8 @@ cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
   const size_t smem = sizeof(SmemQ4<CG, PACK>);
   // CTAs take parts of units (us; dealt / by unit): 2 units of 17 pages 10.3 / 6.8, 64 of 33 13.9 / 10.4, 128 of 17 14.5 /
   // 11.1, 256 of 5 13.4 / 8.3, 400 of 17 24.5 / 18.5.  Not where parts are long, as lists may then be of very different
-  // lengths: 61 of 0 to 129 27 / 33; but there the kernel, which counts them, does where they are not: 64 of 129 26.1 / 25.3.
+  // lengths: 61 of 0 to 129 27 / 33; but there the kernel, which counts them, does where they are not: 64 of 129 26.0 / 25.7,
+  // a step with 128 of 65 32.4 / 31.1.
   // A part's pages: the CTAs' time grows with them and the merge's with the parts, so with the root of the length
   // (129 pages in 16, 26, 33 parts 9.8, 10.2, 10.5; 500 in 16, 32, 63: 18.0, 15.3, 15.6).
   const int n = p.a.sel_stride;
@@ -793,19 +797,21 @@ cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
   p.parts = static_cast<int>(min(int64_t(n + p.part_pages - 1) / p.part_pages, max(slots / U, int64_t(1))));
   const int64_t most = int64_t(kUnitPages) * p.parts * (U > C::kWindow ? 2 : 1);   // finding one's pages among more is slow
   if (U <= slots && n <= most)
-    return launch_pdl(attn_q4_kernel<CG, PACK, true>, dim3(static_cast<unsigned>(U * p.parts)), block, smem, st, p);
-  if (U > C::kWindow || U * p.parts * 5 < slots * 4) p.parts = 0;   // a fifth of the CTAs would have nothing
+    return launch_pdl(attn_q4_kernel<CG, PACK, kByUnit>, dim3(static_cast<unsigned>(U * p.parts)), block, smem, st, p);
+  const bool fill = U <= C::kWindow && U * p.parts * 5 >= slots * 4;   // four fifths of the CTAs
   const int64_t want = (U * p.a.sel_stride + kCtaPages - 1) / kCtaPages;
-  return launch_pdl(attn_q4_kernel<CG, PACK, false>, dim3(static_cast<unsigned>(min(want, slots))), block, smem, st, p);
+  return launch_pdl(fill ? attn_q4_kernel<CG, PACK, kEither> : attn_q4_kernel<CG, PACK, kDealt>, dim3(static_cast<unsigned>(min(want, slots))), block, smem, st, p);
 }
 
 template <int CG, bool PACK>
 cudaError_t set_attr() {
   static_assert(Cfg<CG, PACK>::kCtasPerSm * (sizeof(SmemQ4<CG, PACK>) + 1024) <= 233472, "shared memory");
   const int bytes = static_cast<int>(sizeof(SmemQ4<CG, PACK>));
-  const cudaError_t e = cudaFuncSetAttribute(attn_q4_kernel<CG, PACK, true>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
-  return e != cudaSuccess ? e : cudaFuncSetAttribute(attn_q4_kernel<CG, PACK, false>,
-                                                     cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+  for (auto kernel : {attn_q4_kernel<CG, PACK, kDealt>, attn_q4_kernel<CG, PACK, kEither>, attn_q4_kernel<CG, PACK, kByUnit>}) {
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
 }  // namespace

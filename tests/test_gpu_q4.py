@@ -264,13 +264,17 @@ def test_attention_bad_entries_are_skipped():
     check(out, lse, ref.attention(qx, c.blob, c.gk, c.gv, c.pt, good, gn, c.L))
 
 
-def test_attention_page_ids_past_the_positions():
-    """Page ids whose tokens would lie past 2^31 are bad entries, though the table goes on."""
+def test_attention_page_tables_past_the_positions():
+    """A table with more pages than positions below 2^31 is refused, one with as many is not."""
     c = Cache(1, 1, 1, [64], seed=23)
     x, q = queries(1, 4)
-    wide = torch.zeros(1, (1 << 25) + 8, dtype=torch.int32, device=DEV)
+    wide = torch.zeros(1, (1 << 25) + 1, dtype=torch.int32, device=DEV)
     out, lse = torch.zeros(1, 4, 128, device=DEV), torch.zeros(1, 4, device=DEV)
-    spkv.sparse_decode_attn(c.handle, q, wide, i32([[[0, 1 << 25, (1 << 25) + 1]]]), i32([[3]]), i32([64]), out, lse)
+    with pytest.raises(spkv.SpkvError) as e:
+        spkv.sparse_decode_attn(c.handle, q, wide, i32([[[0]]]), i32([[1]]), i32([64]), out, lse)
+    assert e.value.status == -1
+    wide = wide[:, 1:].contiguous()
+    spkv.sparse_decode_attn(c.handle, q, wide, i32([[[0, (1 << 25) - 1, 1 << 25]]]), i32([[3]]), i32([64]), out, lse)
     assert spkv.get_device_error(c.handle)[1] == spkv.DEVERR["PAGE_ID"]
     c.pt[:] = 0
     check(out, lse, ref.attention(x, c.blob, c.gk, c.gv, c.pt, np.zeros((1, 1, 1), int), np.array([[1]]), c.L))
