@@ -377,8 +377,8 @@ struct Cfg {
   static_assert(L % NS == 0 && L % TEAMS == 0, "barriers");
 };
 
-// Pages of a CTA where they are dealt, at least (few units have so few: 4 spares 32 units of 9 pages 4 us, costs one of
-// 500 pages 5), of a part of a unit, at least, and of a part, at most, where the launch alone lets CTAs take units.
+// Pages of a CTA where they are dealt, at least; of a part of a unit, at least; and of a part, at most, where the launch
+// alone lets CTAs take units.
 constexpr int kCtaPages = 8, kPartPages = 4, kUnitPages = 16;
 // Places between two units' pages where the pages are dealt: what a unit's end (the warps waiting for one another,
 // merges, the next queries) costs the CTA that meets it.  Without them such CTAs end 2 to 5 us after the others.
@@ -799,8 +799,12 @@ cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
   if (U <= slots && n <= most)
     return launch_pdl(attn_q4_kernel<CG, PACK, kByUnit>, dim3(static_cast<unsigned>(U * p.parts)), block, smem, st, p);
   const bool fill = U <= C::kWindow && U * p.parts * 5 >= slots * 4;   // four fifths of the CTAs
-  const int64_t want = (U * p.a.sel_stride + kCtaPages - 1) / kCtaPages;
-  return launch_pdl(fill ? attn_q4_kernel<CG, PACK, kEither> : attn_q4_kernel<CG, PACK, kDealt>, dim3(static_cast<unsigned>(min(want, slots))), block, smem, st, p);
+  // Few long lists are not dealt to all CTAs (8, 16, 24 pages each: one list of 1000 24.0, 19.7, 20.1 us, one of 2000 39.5,
+  // 26.4, 25.7, four of 900 27.7, 22.0, 20.1), many short ones are (256 of 17: 17.2 with 8, 22.4 with 24).
+  const int least = max(kCtaPages, p.part_pages);
+  const int64_t want = max((U * n + least - 1) / least, fill ? U * p.parts : 0);   // each part has its CTA
+  const dim3 grid(static_cast<unsigned>(min(want, slots)));
+  return launch_pdl(fill ? attn_q4_kernel<CG, PACK, kEither> : attn_q4_kernel<CG, PACK, kDealt>, grid, block, smem, st, p);
 }
 
 template <int CG, bool PACK>
