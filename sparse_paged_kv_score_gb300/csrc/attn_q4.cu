@@ -427,7 +427,7 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
 // units of 65 pages take 0.5 us more.)
 //
 // Measured (GB300): 256 units of 65 pages, 4 heads 37 us = 153 MB at 4.1 TB/s (0.61 of the copy rate); 64 units of
-// 129 pages, 5 heads 25 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
+// 129 pages, 5 heads 26 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
 // the first pages are there (lengths, lists, page table and page read one after the other), 25 us at 6.3 TB/s, and
 // 4 us from the first CTA's end to the last's, merges included.  The other two are bound by instructions (1165 a
 // page and warp for up to 4 heads, 1411 for 8: half unpack and scale codes) and by the same ends.
