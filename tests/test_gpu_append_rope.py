@@ -478,3 +478,46 @@ def test_refused_arguments():
     assert spkv.get_device_error(b.cache) == (0, 0)
     b.call(**rot)
     b.check(b.expect())
+
+
+@pytest.mark.parametrize("q4", FORMATS)
+def test_offsets_past_32_bits(q4):
+    """A pool of more than 2^32 bytes, its last pages used: bit for bit what a small pool holds, gives and attends."""
+    b = Batch(q4, [70], [130], 8, 1, seed=30, fused=True)
+    n = (1 << 32) // (9216 if q4 else 16384) + 40
+    pt = n - 1 - np.arange(b.np_max, dtype=np.int32)[None]
+    cnt = torch.zeros(n, dtype=torch.int32, device=DEV)
+    ksum = torch.zeros(1, n, 4, 128, device=DEV)
+    old, new = torch.from_numpy(b.pt[0].astype(np.int64)).to(DEV), torch.from_numpy(pt[0].astype(np.int64)).to(DEV)
+    cnt[new] = b.cnt_d[old]
+    if q4:
+        pools = [torch.zeros(1, n, 9216, dtype=torch.uint8, device=DEV)]
+        small = [b.pool]
+    else:
+        pools = [torch.zeros(1, n, 64, 128, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        small = [b.kp, b.vp]
+    for big, sm in zip(pools, small):
+        big[:, new] = sm[:, old]
+    if q4:
+        cache = spkv.paged_kv_create_q4(pools[0], f32(b.gk), f32(b.gv), ksum, cnt, max_units=4)
+    else:
+        cache = spkv.paged_kv_create(*pools, ksum, cnt, max_units=4)
+    q_out = torch.zeros_like(b.q_out)
+    spkv.paged_kv_append_rope(cache, b.kd, b.vd, i32(b.L), i32(pt), row_first=i32(b.first), q=b.qd, q_out=q_out, cos_sin=f32(b.tab))
+    b.call()
+    assert spkv.get_device_error(cache) == (0, 0)
+    b.check(b.expect())
+    assert torch.equal(q_out, b.q_out) and torch.equal(ksum[:, new], b.ksum[:, old]) and torch.equal(cnt[new], b.cnt_d[old])
+    for big, sm in zip(pools, small):
+        assert torch.equal(big[:, new], sm[:, old])
+    outs = []
+    for c, table in ((cache, pt), (b.cache, b.pt)):
+        out, lse = torch.zeros(1, 8, 128, device=DEV), torch.zeros(1, 8, device=DEV)
+        spkv.sparse_decode_attn(c, q_out[-1:].contiguous(), i32(table), i32([[[0, 1, 2, 3]]]), i32([[4]]), i32(b.L), out, lse)
+        outs.append((out, lse))
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+    if q4:
+        pages = [torch.zeros(1, 4, 64, 128, dtype=torch.bfloat16, device=DEV) for _ in range(4)]
+        spkv.paged_kv_unpack_q4(cache, i32(pt[0, :4]), pages[0], pages[1])
+        spkv.paged_kv_unpack_q4(b.cache, i32(b.pt[0, :4]), pages[2], pages[3])
+        assert torch.equal(pages[0], pages[2]) and torch.equal(pages[1], pages[3])
