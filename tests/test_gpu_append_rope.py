@@ -246,6 +246,25 @@ def test_q4_tiny_and_huge_values():
         assert np.array_equal(b.pool.cpu().numpy(), b.blob)
 
 
+@pytest.mark.parametrize("g", [2.0 ** -118, 2.0 ** -102, 2.0 ** -97, 1.0, 0.7, 2.0 ** 95, 2.0 ** 101])
+def test_q4_ties(g):
+    """Values on the ties between codes, and a bf16 step beside them, for factors up to the ends of fp32."""
+    b = Batch(True, [0], [64], 2, 1, seed=31, rope=False)
+    b.gk[:] = b.gv[:] = g
+    b.cache = spkv.paged_kv_create_q4(b.pool, f32(b.gk), f32(b.gv), b.ksum, b.cnt_d, max_units=64)
+    rng = np.random.default_rng(5)
+    ties = np.array([0, .25, .5, .75, 1, 1.25, 1.5, 1.75, 2, 2.5, 3, 3.5, 4, 5, 6, 6])
+    x = rng.permuted(np.tile(ties, (64, 3, 8)).reshape(64, 3, 8, 16), axis=-1) * rng.choice([-1, 1], (64, 3, 8, 16))
+    x = x * 2.0 ** rng.integers(-6, 6, (64, 3, 8, 1)) * np.float64(np.float32(g))
+    x = x.reshape(64, 3, 128) * (1 + rng.choice([-2.0 ** -8, 0, 0, 0, 2.0 ** -7], (64, 3, 128)))
+    b.x[:, 1:] = 0
+    b.x[:, 2:4] = ref.bf16(x[:, :2].astype(np.float32))
+    b.kd, b.vd = bf(ref.bf16_bits(b.x[:, 2:3])), bf(ref.bf16_bits(b.x[:, 3:4]))
+    b.call()
+    b.expect()
+    assert np.array_equal(b.pool.cpu().numpy(), b.blob)
+
+
 def test_q4_held_values_are_near():
     """In 64 bits: a held value is off by at most half the code's step and the scale's rounding.
 
