@@ -30,13 +30,12 @@ With the cache held in 4 bits, and the rotary positions applied where rows are a
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
 
 import numpy as np
 import torch
 
-from ._abi import DEVERR, SpkvDesc, SpkvDescQ4, SpkvError, SpkvPageDir, SpkvRope, check, load
+from ._abi import DEVERR, ROPE, SpkvDesc, SpkvDescQ4, SpkvError, SpkvPageDir, check, load
 
 __all__ = ["PagedKVCache", "paged_kv_create", "paged_kv_append", "score_blocks", "decode_append_score",
            "select_topk",
@@ -182,12 +181,7 @@ def paged_kv_create_q4(kv_pool, k_scale, v_scale, ksum, page_cnt, max_units: int
     return PagedKVCacheQ4(kv_pool, k_scale, v_scale, ksum, page_cnt, max_units, stream)
 
 
-_NO_GUARD = contextlib.nullcontext()
-
-
-def _on(device):
-    """Makes ``device`` the current one where it is not (a torch.cuda.device costs 1.3 us a call)."""
-    return _NO_GUARD if torch._C._cuda_getDevice() == device.index else torch.cuda.device(device)
+# The checks below cost what they do on every call: a decode step's append takes 4 us on the GPU.
 
 
 def _same_device(device, **tensors) -> None:
@@ -196,25 +190,25 @@ def _same_device(device, **tensors) -> None:
             raise ValueError(f"{name}: must be on {device}, the cache's device")
 
 
-def _on_device(x: torch.Tensor, dtype, name: str, shape, device) -> int:
-    """_t of a tensor on ``device``; one look at its index, where the rest is as it should be."""
-    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == device.index and x.is_contiguous()
-            and x.shape == shape):
+def _at(x: torch.Tensor, dtype, name: str, shape, index: int) -> int:
+    """_t of a tensor on CUDA device ``index``."""
+    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == index and x.is_contiguous()
+            and x.shape == shape and index >= 0):
         return x.data_ptr()
     at = _t(x, dtype, name, shape)
-    _same_device(device, **{name: x})
+    _same_device(torch.device("cuda", index), **{name: x})
     return at
 
 
-def _rows(x: torch.Tensor, name: str, n: int, heads: int, device):
-    """Address and row stride of bf16 rows [n][heads][128] on ``device`` whose rows may lie apart (a slice of a
-    wider projection's output)."""
+def _rows(x: torch.Tensor, name: str, n: int, heads: int, index: int):
+    """Address and row stride of bf16 rows [n][heads][128] on CUDA device ``index`` whose rows may lie apart (a
+    slice of a wider projection's output)."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if x.dtype is not torch.bfloat16:
         raise TypeError(f"{name}: expected {torch.bfloat16}, got {x.dtype}")
-    if x.get_device() != device.index or not x.is_cuda:
-        raise ValueError(f"{name}: must be a CUDA tensor on {device}, the cache's device")
+    if x.get_device() != index or index < 0:
+        raise ValueError(f"{name}: must be a CUDA tensor on the cache's device")
     if x.shape != (n, heads, HEAD_DIM):
         raise ValueError(f"{name}: expected shape {(n, heads, HEAD_DIM)}, got {tuple(x.shape)}")
     row, head, one = x.stride()
@@ -235,7 +229,7 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
     positions in the context); with several axes pair_axis lists each pair's axis."""
     n, Hk = k_new.shape[0], cache.n_kv_heads
     B, np_max = page_table.shape
-    dev = cache.tensors[0].device
+    dev = cache.tensors[0].get_device()
     kp, ks = _rows(k_new, "k_new", n, Hk, dev)
     vp, vs = _rows(v_new, "v_new", n, Hk, dev)
     rope, axes, qp, qs, Hq, qo = None, None, None, 0, 0, None
@@ -249,8 +243,9 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
         elif n_axes > 1:
             raise ValueError("pair_axis: needed with several axes")
         n_pos = cos_sin.shape[0]
-        rope = SpkvRope(_on_device(cos_sin, torch.float32, "cos_sin", (n_pos, HEAD_DIM), dev), n_pos, n_axes, axes, None if pos is None
-                        else _on_device(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (n, n_axes), dev))
+        rope = ROPE.pack(_at(cos_sin, torch.float32, "cos_sin", (n_pos, HEAD_DIM), dev), n_pos, n_axes,
+                          0 if axes is None else ctypes.addressof(axes),
+                          0 if pos is None else _at(pos, torch.int32, "pos", (n,) if pos.dim() == 1 else (n, n_axes), dev))
     elif pos is not None or pair_axis is not None or q is not None:
         raise ValueError("pos, pair_axis and q are given with cos_sin")
     if q is not None:
@@ -258,13 +253,17 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
         qp, qs = _rows(q, "q", n, Hq, dev)
         if q_out is None:
             raise ValueError("q_out: needed with q")
-        qo = _on_device(q_out, torch.bfloat16, "q_out", (n, Hq, HEAD_DIM), dev)
-    first = None if row_first is None else _on_device(row_first, torch.int32, "row_first", (B + 1,), dev)
-    lens = _on_device(seq_len, torch.int32, "seq_len", (B,), dev)
-    table = _on_device(page_table, torch.int32, "page_table", (B, np_max), dev)
-    with _on(dev):
-        check("paged_kv_append_rope", load().paged_kv_append_rope(
-            cache.handle, kp, ks, vp, vs, n, B, first, lens, table, np_max, rope, qp, qs, Hq, qo, _stream(stream)))
+        qo = _at(q_out, torch.bfloat16, "q_out", (n, Hq, HEAD_DIM), dev)
+    first = None if row_first is None else _at(row_first, torch.int32, "row_first", (B + 1,), dev)
+    lens = _at(seq_len, torch.int32, "seq_len", (B,), dev)
+    table = _at(page_table, torch.int32, "page_table", (B, np_max), dev)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return paged_kv_append_rope(cache, k_new, v_new, seq_len, page_table, row_first, q, q_out, cos_sin, pos, pair_axis,
+                                        stream)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    check("paged_kv_append_rope", load().paged_kv_append_rope(
+        cache.handle, kp, ks, vp, vs, n, B, first, lens, table, np_max, rope, qp, qs, Hq, qo, st))
 
 
 def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
@@ -272,11 +271,14 @@ def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
     (rows at and behind a page's count are left as they are)."""
     n = pages.shape[0]
     shp = (cache.n_kv_heads, n, PAGE, HEAD_DIM)
-    dev = cache.tensors[0].device
-    args = (_on_device(pages, torch.int32, "pages", (n,), dev), n, _on_device(k_out, torch.bfloat16, "k_out", shp, dev),
-            _on_device(v_out, torch.bfloat16, "v_out", shp, dev))
-    with _on(dev):
-        check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(cache.handle, *args, _stream(stream)))
+    dev = cache.tensors[0].get_device()
+    at = _at(pages, torch.int32, "pages", (n,), dev)
+    k, v = _at(k_out, torch.bfloat16, "k_out", shp, dev), _at(v_out, torch.bfloat16, "v_out", shp, dev)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return paged_kv_unpack_q4(cache, pages, k_out, v_out, stream)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(cache.handle, at, n, k, v, st))
 
 
 def paged_kv_append(cache: PagedKVCache, phys_page, tok_in_page, k_new, v_new, stream=None):

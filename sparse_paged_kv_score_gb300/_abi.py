@@ -7,6 +7,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 SO_PATH = os.path.join(_HERE, "libspkv.so")
@@ -39,10 +40,8 @@ class SpkvDescQ4(ctypes.Structure):
                 ("ksum", _vp), ("page_cnt", _vp), ("max_units", ctypes.c_int32), ("ksum_bf16", ctypes.c_int32)]
 
 
-class SpkvRope(ctypes.Structure):
-    _fields_ = [("cos_sin", _vp), ("n_pos", ctypes.c_int64), ("n_axes", ctypes.c_int32),
-                ("pair_axis", ctypes.POINTER(ctypes.c_uint8)), ("pos", _vp)]
-
+# spkv_rope: cos_sin, n_pos, n_axes, pair_axis, pos (packing takes a fifth of building a ctypes.Structure)
+ROPE = struct.Struct("@PqiPP")
 
 _pd = ctypes.POINTER(SpkvPageDir)
 
@@ -50,7 +49,7 @@ SIGNATURES = {
     "paged_kv_create": ([ctypes.POINTER(SpkvDesc), _vp, ctypes.POINTER(_vp)], _i32),
     "paged_kv_append": ([_vp, _vp, _vp, _vp, _vp, _i32, _vp], _i32),
     "paged_kv_create_q4": ([ctypes.POINTER(SpkvDescQ4), _vp, ctypes.POINTER(_vp)], _i32),
-    "paged_kv_append_rope": ([_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i32, ctypes.POINTER(SpkvRope), _vp,
+    "paged_kv_append_rope": ([_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp,
                               _i64, _i32, _vp, _vp], _i32),
     "paged_kv_unpack_q4": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
     "score_blocks": ([_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
