@@ -15,7 +15,6 @@
 // Bound by latency and instructions: a CTA waits for the look-ups, for its rows, and at the barrier in front of the
 // sums.
 #include "q4.cuh"
-#include "summary.cuh"
 
 namespace spkv {
 namespace {
