@@ -798,7 +798,8 @@ cudaError_t launch_one(const spkv_cache* c, AttnQ4Params p, cudaStream_t st) {
   const int64_t most = int64_t(kUnitPages) * p.parts * (U > C::kWindow ? 2 : 1);   // finding one's pages among more is slow
   if (U <= slots && n <= most)
     return launch_pdl(attn_q4_kernel<CG, PACK, kByUnit>, dim3(static_cast<unsigned>(U * p.parts)), block, smem, st, p);
-  const bool fill = U <= C::kWindow && U * p.parts * 5 >= slots * 4;   // four fifths of the CTAs
+  // Four fifths of the CTAs; no more units than CTAs, which only a device with few SMs can have here.
+  const bool fill = U <= C::kWindow && U <= slots && U * p.parts * 5 >= slots * 4;
   // Few long lists are not dealt to all CTAs (8, 16, 24 pages each: one list of 1000 24.0, 19.7, 20.1 us, one of 2000 39.5,
   // 26.4, 25.7, four of 900 27.7, 22.0, 20.1), many short ones are (256 of 17: 17.2 with 8, 22.4 with 24).
   const int least = max(kCtaPages, p.part_pages);
