@@ -25,8 +25,8 @@ def build(out_dir: str) -> str:
 def run(fake: str, program: str) -> str:
     """Output of a child's `program`, which begins with `import fake_cuda` done and the fake loaded as `f`."""
     head = f"import sys; sys.path.insert(0, {HERE!r}); import fake_cuda; f = fake_cuda.Library({fake!r})\n"
-    r = subprocess.run([sys.executable, "-c", head + program], capture_output=True, text=True, timeout=300)
-    assert r.returncode == 0, r.stderr
+    r = subprocess.run([sys.executable, "-X", "faulthandler", "-c", head + program], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, f"status {r.returncode}\n{r.stderr}"
     return r.stdout
 
 
