@@ -116,14 +116,17 @@ int launch_sparse(spkv_cache_t c, const AttnParams& p, int grid, void* stream) {
 }  // namespace
 
 namespace spkv {
-cudaError_t init_kernel_attributes() {
+cudaError_t init_kernel_attributes(bool q4) {
   cudaError_t e;
-  if ((e = attn_init_attributes()) != cudaSuccess) return e;
+  if (q4) {
+    if ((e = attn_q4_init_attributes()) != cudaSuccess) return e;
+  } else {
+    if ((e = attn_init_attributes()) != cudaSuccess) return e;
+    if ((e = prefill_init_attributes()) != cudaSuccess) return e;
+    if ((e = colscore_init_attributes()) != cudaSuccess) return e;
+  }
   if ((e = select_init_attributes()) != cudaSuccess) return e;
   if ((e = fused_init_attributes()) != cudaSuccess) return e;
-  if ((e = prefill_init_attributes()) != cudaSuccess) return e;
-  if ((e = colscore_init_attributes()) != cudaSuccess) return e;
-  if ((e = attn_q4_init_attributes()) != cudaSuccess) return e;
   return resid_init_attributes();
 }
 }  // namespace spkv
@@ -172,7 +175,7 @@ static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scal
     return SPKV_ECUDA;
   }
   c->attn_grid = c->sm_count;
-  if (spkv::init_kernel_attributes() != cudaSuccess) {
+  if (spkv::init_kernel_attributes(pool4 != nullptr) != cudaSuccess) {
     delete c;
     return SPKV_ECUDA;
   }

@@ -65,9 +65,10 @@ cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, 
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
 
-// Sets the dynamic shared-memory limits of every kernel once (at handle creation), so that no
-// launch path calls cudaFuncSetAttribute and every call can be captured in a CUDA graph.
-cudaError_t init_kernel_attributes();
+// Sets the dynamic shared-memory limits of the kernels that a handle's calls launch, a 4-bit one's (q4) or a
+// bf16 one's, at its creation (which loads them), so that no launch path calls cudaFuncSetAttribute and every
+// call can be captured in a CUDA graph.
+cudaError_t init_kernel_attributes(bool q4);
 
 // Parameters of the split-K attention kernel (sparse and lazy forms).
 struct AttnParams {

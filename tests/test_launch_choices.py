@@ -48,3 +48,17 @@ def test_every_part_of_a_unit_has_its_cta(fake, sms):
             assert grid >= U * parts, (m, U, n)
         seen.add(mode)
     assert seen == {0, 1, 2}
+
+
+def test_a_bf16_handle_prepares_no_4bit_kernel(fake):
+    """Creating a handle loads the kernels that its own calls launch, not the other format's, a later one's too."""
+    program = """
+import json
+a, b, c = [f.handle(q4, 2) and f.events() for q4 in (False, True, False)]
+print(json.dumps([a, b, c]))
+"""
+    bf16, q4, again = json.loads(fake_cuda.run(fake, program))
+    sets = [{e.split()[1] for e in x if e.startswith("set ")} for x in (bf16, q4, again)]
+    assert not any("attn_q4" in name for name in sets[0] | sets[2])
+    assert len([name for name in sets[1] if "attn_q4" in name]) == 9 and not any("prefill" in name for name in sets[1])
+    assert sets[0] == sets[2] and "?" not in sets[0] | sets[1]
