@@ -1,6 +1,6 @@
 // A CUDA runtime that runs nothing and writes down what the library asks of it, for the tests of launch
 // choices and refusals that need no GPU.  Loaded with global symbols in front of libspkv.so, in a process of
-// its own.  Every allocation is host memory, every copy and launch a line of the log.
+// its own.  Every allocation is host memory; kernels prepared and launched are lines of the log.
 #include <cstdlib>
 #include <cstring>
 #include <map>
@@ -64,6 +64,12 @@ cudaError_t cudaMemsetAsync(void* p, int v, size_t n, cudaStream_t) {
   std::memset(p, v, n);
   return cudaSuccess;
 }
+cudaError_t cudaMemset(void* p, int v, size_t n) { return cudaMemsetAsync(p, v, n, nullptr); }
+cudaError_t cudaMemcpy(void* to, const void* from, size_t n, cudaMemcpyKind) {
+  std::memcpy(to, from, n);
+  return cudaSuccess;
+}
+cudaError_t cudaHostGetDevicePointer(void**, void*, unsigned) { return cudaErrorInvalidValue; }   // not pinned
 cudaError_t cudaGetDriverEntryPointByVersion(const char*, void** f, unsigned, unsigned long long,
                                              cudaDriverEntryPointQueryResult* q) {
   *f = reinterpret_cast<void*>(encode);

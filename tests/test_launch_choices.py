@@ -62,3 +62,52 @@ print(json.dumps([a, b, c]))
     assert not any("attn_q4" in name for name in sets[0] | sets[2])
     assert len([name for name in sets[1] if "attn_q4" in name]) == 9 and not any("prefill" in name for name in sets[1])
     assert sets[0] == sets[2] and "?" not in sets[0] | sets[1]
+
+
+def test_calls_for_bf16_pools_refuse_a_4bit_handle(fake):
+    """Every entry point that reads or writes bf16 pages: SPKV_EUNSUPPORTED on a 4-bit handle, nothing launched;
+    the same arguments pass on a bf16 handle (where a host pool that is not pinned ends the retrieval)."""
+    program = """
+import ctypes, json
+P = 4096
+pd = f.abi.SpkvPageDir()
+pd.dir, pd.dev_segs, pd.host_chunks, pd.n_dir, pd.seg_shift, pd.n_dev_segs, pd.n_host_segs = P, P, P, 1, 6, 1, 1
+words = (ctypes.c_int32 * 2)(0, 1)
+plan = ctypes.c_void_p()
+calls = dict(
+    paged_kv_append=(P, P, P, P, 1, None),
+    decode_append_score=(P, P, P, 1, 8, P, 4, P, P, None),
+    lazy_rope_decode_attn=(P, 1, 8, P, P, 2, P, 4, P, 1, 1e4, P, P, None),
+    lazy_rope_prefill_attn=(P, 1, 2, 8, P, P, 2, P, 4, P, 1, 1e4, P, P, None),
+    lazy_rope_prefill_step=(P, 1, 2, 8, P, P, 2, P, 4, P, P, 1, 1e4, P, P, None),
+    lazy_alibi_prefill_attn=(P, 1, 2, 8, P, P, 2, P, 4, P, P, 1, P, P, P, None),
+    attn_column_scores=(P, 1, 2, 8, P, 4, P, P, None),
+    attn_column_scores_lse=(P, P, 1, 2, 8, P, 4, P, P, None),
+    retrieve_pages=(P, P, 8, P, 4, 1, P, P, P, P, P, 4, 4, None),
+    retrieve_pages_dir=(P, P, 8, ctypes.byref(pd), 4, 1, P, P, P, P, P, 4, 4, None),
+    lazy_docs_plan_create=(1, 8, words, 1, 1, words, ctypes.byref(plan)),
+)
+got = {}
+for name, args in calls.items():
+    got[name] = []
+    for q4 in (True, False):
+        h = f.handle(q4, 2)
+        f.events()
+        status = getattr(f.lib, name)(h, *args)
+        got[name].append([status, len(f.events())])
+name = "lazy_rope_decode_attn_docs"
+got[name] = []
+for h in (f.handle(True, 2), h):    # the last: the plan's
+    f.events()
+    status = f.lib.lazy_rope_decode_attn_docs(h, plan, P, P, P, P, P, 1e4, P, P, None)
+    got[name].append([status, len(f.events())])
+print(json.dumps(got))
+"""
+    got = json.loads(fake_cuda.run(fake, program))
+    assert len(got) == 12
+    for name, (q4, bf16) in got.items():
+        assert q4 == [-6, 0], name
+        if name.startswith("retrieve"):
+            assert bf16 == [-1, 0], name
+        else:
+            assert bf16[0] == 0 and bf16[1] >= (name != "lazy_docs_plan_create"), (name, bf16)
