@@ -171,7 +171,9 @@ typedef struct {
  * sparse_decode_attn, _slots, _dir, with the arguments they have for a bf16 handle; the other calls,
  * which read or write bf16 pages, return SPKV_EUNSUPPORTED (paged_kv_unpack_q4 gives them such pages).
  * The handle is used where the device is current that was so at its creation, and the attention takes an
- * 8-byte aligned out, np_max <= 2^25 and B * n_kv_heads * (sel_stride + 8) < 2^31 (else SPKV_EINVAL). */
+ * 8-byte aligned out, np_max <= 2^25 and B * n_kv_heads * (sel_stride + 8) < 2^31 (else SPKV_EINVAL).  Its
+ * products take a query's dims to within 2^-38 of the row's largest magnitude; dims within 2^30 of that one
+ * are taken exactly. */
 int paged_kv_create_q4(const spkv_desc_q4* desc, void* stream, spkv_cache_t* out);
 
 /* Rotary positions of paged_kv_append_rope.

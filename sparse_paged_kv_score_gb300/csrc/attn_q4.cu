@@ -6,9 +6,11 @@
 // in one pass with a running maximum and sum.
 //
 // The products run on mma.sync m16n8k16 in f16 with fp32 accumulators, keys (then value dims) as M
-// and the query heads as N.  Nothing is lost on the way in: a code times its e4m3 scale has at most
-// six significant bits, so f16 holds it exactly, and a query row is scaled by a power of two into
-// f16's range (its bf16 has 8 bits); the weights are split into f16 hi + lo parts (22 bits).
+// and the query heads as N.  A code times its e4m3 scale has at most six significant bits, so f16 holds
+// it exactly.  A query row is scaled by a power of two that takes its largest dim into [2^13, 2^14): dims
+// within 30 powers of two of that one keep their 8 bits, smaller ones are off by at most f16's half step,
+// 2^-38 of the largest (a row of bf16 subnormals becomes zeros: with g <= 2^64 its scores are below 2^-40).
+// The weights are split into f16 hi + lo parts (22 bits).
 #include <math_constants.h>
 
 #include <cmath>

@@ -50,6 +50,30 @@ def test_lists_in_any_order(Hq, Hk, pages):
         assert torch.equal(first[0], again[0]) and torch.equal(first[1], again[1])
 
 
+@pytest.mark.parametrize("Hq,Hk", [(4, 1), (12, 1)])
+@pytest.mark.parametrize("wide,exact", [(30, True), (34, False), (44, False)])
+def test_queries_of_a_wide_range(Hq, Hk, wide, exact):
+    """Sixteen dims 2^wide times the others, where the keys are zero.  A query row goes into f16 with its largest dim in
+    [2^13, 2^14): dims within 30 powers of two of that one keep all 8 bits (f16 holds 8 bits down to 2^-17), a smaller one
+    is off by half of f16's smallest number, 2^-25, at most: 2^-38 of the largest."""
+    c = Cache(Hk, 2, 6, [380, 200], seed=51, junk=True)
+    c.blob[:, :, ref.KC[:, :8]] = 0
+    c.pool.copy_(torch.from_numpy(c.blob))
+    sel, n = c.select(6, np.random.default_rng(3))
+    rng = np.random.default_rng(wide)
+    qx = rng.choice([-1, 1], (2, Hq, 128)) * (rng.uniform(1, 1.9, (2, Hq, 128)) if exact else rng.standard_normal((2, Hq, 128)))
+    qx[:, :, :16] *= 2.0 ** wide
+    qx[:, :, 3] = 2.0 ** wide
+    qx = ref.bf16(qx.astype(np.float32))
+    out, lse = c.attend(bf(ref.bf16_bits(qx)), sel, n)
+    o, l, eo, el = ref.attention(qx, c.blob, c.gk, c.gv, c.pt, sel, n, c.L)
+    if not exact:
+        k, v = (np.abs(np.nan_to_num(ref.rows(c.blob, keys))) for keys in (True, False))
+        dx = 2.0 ** -38 * np.abs(qx).max() * (k * c.gk[:, None, None, None]).sum(-1).max() / np.sqrt(128)
+        eo, el = eo + 2 * dx * (v * c.gv[:, None, None, None]).max(), el + dx
+    check(out, lse, (o, l, eo, el))
+
+
 @pytest.mark.parametrize("Hq,Hk", [(8, 2), (6, 1), (16, 1), (13, 1)])
 @pytest.mark.parametrize("special", [np.nan, np.inf, -np.inf])
 @pytest.mark.parametrize("L", [3, 700])
