@@ -78,7 +78,7 @@ constexpr float kShift = 7.f, kSlack = 8.f;
 
 // A warp's state of a unit in shared memory: for each query head the reference (-inf: no token), the sum
 // of weights and the weighted sum of values, its dims 16 r + 2 i (+ 1) at places 16 i + 2 r (+ 1) of a
-// padded row, so that the stores meet no bank twice.  It takes the place of the page that it ends with.
+// padded row, so that the stores meet no bank twice.
 constexpr int kRow = kHeadDim + 4;
 template <int COLS>
 struct State {
@@ -431,8 +431,10 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
 // Measured (GB300): 256 units of 65 pages, 4 heads 37 us = 153 MB at 4.1 TB/s (0.61 of the copy rate); 64 units of
 // 129 pages, 5 heads 26 us; 61 of up to 129 pages, 16 heads 27 us; 2 of 17 pages 7 us.  Of the first 37: 6 us until
 // the first pages are there (lengths, lists, page table and page read one after the other), 25 us at 6.3 TB/s, and
-// 4 us from the first CTA's end to the last's, merges included.  The other two are bound by instructions (1165 a
-// page and warp for up to 4 heads, 1411 for 8: half unpack and scale codes) and by the same ends.
+// 4 us from the first CTA's end to the last's, merges included.  The next two are bound by the latency of a page in
+// one warp, 1340 to 1370 instructions (half unpack and scale codes) that three warps a scheduler (168 registers) do
+// not hide: they issue in 41 % of the slots, 9 us of it, and the rest waits on fixed latencies, on barriers and for
+// the same ends.
 enum Mode { kDealt, kEither, kByUnit };
 
 template <int CG, bool PACK, Mode MODE>
