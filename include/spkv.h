@@ -170,6 +170,8 @@ typedef struct {
  * score_blocks(_dir), select_topk, resident_setdiff, lru_bucket_update, select_resident_update and
  * sparse_decode_attn, _slots, _dir, with the arguments they have for a bf16 handle; the other calls,
  * which read or write bf16 pages, return SPKV_EUNSUPPORTED (paged_kv_unpack_q4 gives them such pages).
+ * retrieve_pages is one of these: a slot pool in 4 bits is filled by the caller, who copies the 9216 bytes of
+ * each missing page's head to its victim slot and completes the slot list, as retrieve_pages does for bf16.
  * The handle is used where the device is current that was so at its creation, and the attention takes an
  * 8-byte aligned out, np_max <= 2^25 and B * n_kv_heads * (sel_stride + 8) < 2^31 (else SPKV_EINVAL).  Its
  * products take a query's dims to within 2^-38 of the row's largest magnitude; dims within 2^30 of that one

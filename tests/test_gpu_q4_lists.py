@@ -185,3 +185,38 @@ def test_unpack_in_a_graph_and_on_another_stream():
     empty = torch.zeros(2, 0, 64, 128, dtype=torch.bfloat16, device=DEV)
     spkv.paged_kv_unpack_q4(c.handle, i32(np.zeros(0)), empty, empty)
     assert spkv.get_device_error(c.handle) == (0, 0)
+
+
+def test_slots_that_the_caller_fills():
+    """Decode steps over a 4-bit slot pool: the missing pages' bytes copied to their victim slots and the slot list
+    completed by the caller; bit for bit the attention over the whole pool."""
+    B, Hk, Hq, npm, slots, stride = 2, 2, 8, 30, 9, 6
+    U = B * Hk
+    c = Cache(Hk, B, npm, [30 * 64 - 3, 25 * 64 + 1], seed=43)
+    pool = torch.zeros(Hk, B * slots, 9216, dtype=torch.uint8, device=DEV)
+    s = spkv.paged_kv_create_q4(pool, c.gk_d, c.gv_d, None, None, max_units=U)
+    resident = torch.full((U, slots), -1, dtype=torch.int32, device=DEV)
+    ts = torch.full((U, slots), -2 ** 31, dtype=torch.int32, device=DEV)
+    rng = np.random.default_rng(4)
+    brought = 0
+    for t in range(5):
+        sel, n = c.select(stride, rng, rng.integers(1, stride + 1, (B, Hk)))
+        _, q = queries(B, Hq, seed=60 + t)
+        sel_d, n_d = i32(sel), i32(n)
+        missing, slot, victims = (torch.full((U, stride), -1, dtype=torch.int32, device=DEV) for _ in range(3))
+        n_missing, hist = torch.zeros(U, dtype=torch.int32, device=DEV), torch.zeros(U, 64, dtype=torch.int32, device=DEV)
+        spkv.resident_setdiff(s, resident, sel_d, n_d, missing, n_missing, slot)
+        spkv.lru_bucket_update(s, resident, ts, slot, n_d.view(U), missing, n_missing, t, 1, victims, hist)
+        for u in range(U):
+            b, h, k = u // Hk, u % Hk, int(n_missing[u])
+            brought += k
+            to, page = victims[u, :k].long(), missing[u, :k].cpu().numpy()
+            pool[h, b * slots + to] = c.pool[h, torch.from_numpy(c.pt[b, page].astype(np.int64)).to(DEV)]
+            row = slot[u, :int(n[b, h])]
+            row[row < 0] = victims[u, :k]
+        out, lse = torch.zeros(B, Hq, 128, device=DEV), torch.zeros(B, Hq, device=DEV)
+        spkv.sparse_decode_attn_slots(s, q, sel_d, slot.view(B, Hk, stride), n_d, slots, i32(c.L), out, lse)
+        assert spkv.get_device_error(s) == (0, 0)
+        want = c.attend(q, sel, n)
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert brought > 0
