@@ -5,7 +5,9 @@ namespace spkv {
 namespace {
 
 // One CTA per page-head, one thread per dim: sums of each sub-block's valid keys in token order,
-// the codes times their scales first (exact in fp32) and the head's scale once at the end.
+// the codes times their scales first (exact in fp32) and the head's scale once at the end.  Bound by
+// latency, one byte a load and one token after another: 65536 pages of 8 heads 4.4 ms = 3.5 GB (fp32 sums) at
+// 0.8 TB/s, 8.5 times the floor.  It runs once, when a handle is made over a pool that holds rows.
 template <bool BF16>
 __global__ void __launch_bounds__(kHeadDim)
     summary_build_q4_kernel(const uint8_t* __restrict__ pool, const float* __restrict__ k_scale,
