@@ -24,6 +24,7 @@
  *   paged_kv_create_q4   a cache held in 4 bits; paged_kv_append_rope, score_blocks, the selection and
  *                        the three sparse_decode_attn calls work on it
  *   paged_kv_unpack_q4   pages of a 4-bit cache back as bf16 pages
+ *   paged_kv_create_q8, paged_kv_unpack_q8  the same for a cache held in 8 bits, one scale for 16 tokens of a head
  *   score_blocks_dir, sparse_decode_attn_dir, retrieve_pages_dir  the same calls through a
  *                        two-level page directory (spkv_pagemap_* manages one)
  *
@@ -200,7 +201,7 @@ typedef struct {
  * row the key's and the query heads' pairs are rotated, in fp32,
  *   (x_j, x_{j+64}) -> (x_j c - x_{j+64} s, x_{j+64} c + x_j s)
  * by the cos c and sin s of its position; the queries are rounded to bf16 into q_out, the keys (rounded
- * to bf16, or from fp32 to the 4-bit format) and the values go to the cache, page_cnt is raised and
+ * to bf16, or from fp32 to the 4-bit or 8-bit format) and the values go to the cache, page_cnt is raised and
  * the sub-block sums that changed are formed again in paged_kv_append's order (rows in front of the
  * new ones count as held, rows behind them as far as page_cnt says).
  *   k_new, v_new : device bf16, rows k_stride (v_stride) elements apart, each [n_kv_heads][128]
@@ -228,6 +229,42 @@ int paged_kv_append_rope(spkv_cache_t cache, const void* k_new, int64_t k_stride
  *                  page_cnt of a page are left as they are (a handle without page_cnt: all 64 are written)
  * SPKV_EUNSUPPORTED for a bf16 handle, SPKV_EINVAL for another device's. */
 int paged_kv_unpack_q4(spkv_cache_t cache, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream);
+
+/* A cache held in 8 bits.  A sub-block's 16 tokens x 128 dims of one head share one scale, a power of two, keys and
+ * values apart.  With a the largest magnitude of the rows that it holds and E = floor(log2 a) it holds
+ *   s = 2^(E - 6), at least 2^-126;  code c = floor(x / s), -128 .. 127;  value = (c + 1/2) s
+ * so a value is off by at most s / 2 <= a / 128: 8.02 bits a value, 16416 bytes a page-head (bf16: 32768).  A sub-block of
+ * zeros has the scale 0 and holds zeros; one with an infinity or a NaN has a NaN scale and reads back as NaN until its page
+ * is begun again.  Rows that are added to a sub-block can only raise its scale; its codes are then floored again, which
+ * leaves what they would be had all rows come at once: however appends are cut into calls, the cache holds the same.  (Where
+ * rows are overwritten while their sub-block holds others, its scale stays at least what it was.)  Values are exact in bf16,
+ * sub-block sums in fp32.
+ *   kv_pool : [n_kv_heads][n_phys_pages][16416] bytes, 16-byte aligned.  Inside a page-head, with t the token, d the dim and
+ *             u = c + 128 the byte of a code:
+ *     key codes    1024 (t / 8) + 512 ((d / 16) % 2) + 64 (t % 8) + 16 (d / 32) + d % 16
+ *     value codes  8192 + 1024 (t / 8) + 512 ((d / 8) % 2) + 64 (d / 16) + 16 ((t % 8) / 2) + 2 (d % 8) + t % 2
+ *     key scales   16384 + 4 (t / 16), fp32;  value scales  16400 + 4 (t / 16), fp32
+ *   the other fields : as spkv_desc_q4. */
+typedef struct {
+  int32_t n_kv_heads;
+  int32_t head_dim;     /* must be 128 */
+  int32_t page_tokens;  /* must be 64 */
+  int32_t subblock;     /* must be 16 */
+  int64_t n_phys_pages;
+  void* kv_pool;
+  void* ksum;
+  int32_t* page_cnt;
+  int32_t max_units;
+  int32_t ksum_bf16;
+} spkv_desc_q8;
+
+/* paged_kv_create for an 8-bit cache.  What paged_kv_create_q4 says of a 4-bit handle holds for this one: which calls work
+ * on it (paged_kv_unpack_q8 for paged_kv_unpack_q4) and which refuse it, slots (16416 bytes a page's head), devices and the
+ * attention's limits. */
+int paged_kv_create_q8(const spkv_desc_q8* desc, void* stream, spkv_cache_t* out);
+
+/* paged_kv_unpack_q4 for an 8-bit cache; the values are exact. */
+int paged_kv_unpack_q8(spkv_cache_t cache, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream);
 
 /* Block scores, [NOSA] "Method 1", block-wise implementation (two-stage pooling: mean over
  * each 16-token sub-block, max over the 4 sub-blocks of the page) and dual selection

@@ -27,6 +27,10 @@ With the cache held in 4 bits, and the rotary positions applied where rows are a
     score_blocks(cache, q_rot, page_table, seq_len, scores)   # and select_topk, as above
     sparse_decode_attn(cache, q_rot, page_table, sel, n_sel, seq_len, out, lse)
     paged_kv_unpack_q4(cache, pages, k_pages, v_pages)        # bf16 pages for a prefill
+
+and in 8 bits, with a scale for each sub-block of 16 tokens that the append finds by itself:
+
+    cache = paged_kv_create_q8(kv_pool, ksum, page_cnt)       # then the same calls, and paged_kv_unpack_q8
 """
 from __future__ import annotations
 
@@ -35,7 +39,7 @@ import ctypes
 import numpy as np
 import torch
 
-from ._abi import DEVERR, ROPE, SpkvDesc, SpkvDescQ4, SpkvError, SpkvPageDir, check, load
+from ._abi import DEVERR, ROPE, SpkvDesc, SpkvDescQ4, SpkvDescQ8, SpkvError, SpkvPageDir, check, load
 
 __all__ = ["PagedKVCache", "paged_kv_create", "paged_kv_append", "score_blocks", "decode_append_score",
            "select_topk",
@@ -46,11 +50,12 @@ __all__ = ["PagedKVCache", "paged_kv_create", "paged_kv_append", "score_blocks",
            "sparse_decode_attn_noalloc", "pack_page_words", "get_device_error", "SpkvError", "DEVERR",
            "PageMap", "score_blocks_dir", "sparse_decode_attn_dir", "retrieve_pages_dir", "DocPlan",
            "lazy_rope_decode_attn_docs", "PagedKVCacheQ4", "paged_kv_create_q4", "paged_kv_append_rope",
-           "paged_kv_unpack_q4",
+           "paged_kv_unpack_q4", "PagedKVCacheQ8", "paged_kv_create_q8", "paged_kv_unpack_q8",
            "load"]
 
 HEAD_DIM, PAGE, SUBBLOCK = 128, 64, 16
 Q4_PAGE_BYTES = 9216   # one page of one kv head of a 4-bit cache
+Q8_PAGE_BYTES = 16416  # of an 8-bit cache
 
 
 def _stream(stream) -> int:
@@ -181,6 +186,39 @@ def paged_kv_create_q4(kv_pool, k_scale, v_scale, ksum, page_cnt, max_units: int
     return PagedKVCacheQ4(kv_pool, k_scale, v_scale, ksum, page_cnt, max_units, stream)
 
 
+class PagedKVCacheQ8(PagedKVCache):
+    """A handle over a pool held in 8 bits: ``kv_pool`` uint8 [Hk][n_phys][16416] (keys and values of a page-head
+    together with their scales, one for 16 tokens; spkv.h gives the layout).  ``ksum`` and ``page_cnt`` as for
+    :class:`PagedKVCacheQ4`."""
+
+    def __init__(self, kv_pool, ksum, page_cnt, max_units: int = 0, stream=None):
+        self.handle = None
+        if kv_pool.dim() != 3:
+            raise ValueError(f"kv_pool: expected [Hk][n_phys][{Q8_PAGE_BYTES}]")
+        Hk, n_phys = kv_pool.shape[0], kv_pool.shape[1]
+        if ksum is not None and page_cnt is None:
+            raise ValueError("ksum is given with page_cnt")
+        ksum_bf16 = ksum is not None and ksum.dtype == torch.bfloat16
+        self.desc = SpkvDescQ8(Hk, HEAD_DIM, PAGE, SUBBLOCK, n_phys,
+                               _t(kv_pool, torch.uint8, "kv_pool", (Hk, n_phys, Q8_PAGE_BYTES)),
+                               None if ksum is None else _t(ksum, torch.bfloat16 if ksum_bf16 else torch.float32, "ksum",
+                                                            (Hk, n_phys, 4, HEAD_DIM)),
+                               None if page_cnt is None else _t(page_cnt, torch.int32, "page_cnt", (n_phys,)),
+                               int(max_units), int(ksum_bf16))
+        _same_device(kv_pool.device, ksum=ksum, page_cnt=page_cnt)
+        self.n_kv_heads, self.n_phys = Hk, n_phys
+        self.tensors = (kv_pool, ksum, page_cnt)   # keep the buffers alive
+        h = ctypes.c_void_p()
+        with torch.cuda.device(kv_pool.device):
+            check("paged_kv_create_q8", load().paged_kv_create_q8(ctypes.byref(self.desc), _stream(stream),
+                                                                  ctypes.byref(h)))
+        self.handle = h
+
+
+def paged_kv_create_q8(kv_pool, ksum, page_cnt, max_units: int = 0, stream=None) -> PagedKVCacheQ8:
+    return PagedKVCacheQ8(kv_pool, ksum, page_cnt, max_units, stream)
+
+
 # The checks below cost what they do on every call: a decode step's append takes 4 us on the GPU.
 
 
@@ -222,7 +260,7 @@ _PairAxes = ctypes.c_uint8 * (HEAD_DIM // 2)
 
 def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table, row_first=None, q=None, q_out=None,
                          cos_sin=None, pos=None, pair_axis=None, stream=None):
-    """Appends rows k_new, v_new (bf16 [n_rows][Hk][128]; rows may be strided) to a bf16 or 4-bit cache, keys
+    """Appends rows k_new, v_new (bf16 [n_rows][Hk][128]; rows may be strided) to a bf16, 4-bit or 8-bit cache, keys
     rotated by their positions; q (bf16 [n_rows][Hq][128]) rotated into q_out.  row_first int32 [B + 1] gives
     each request's rows (None: one row a request), seq_len counts the new tokens, cos_sin fp32 [n_pos][128] holds
     the cosines and sines of the 64 pairs (None: no rotation).  pos int32 [n_rows] or [n_rows][n_axes] (None: the
@@ -266,9 +304,7 @@ def paged_kv_append_rope(cache: PagedKVCache, k_new, v_new, seq_len, page_table,
         cache.handle, kp, ks, vp, vs, n, B, first, lens, table, np_max, rope, qp, qs, Hq, qo, st))
 
 
-def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
-    """The listed physical pages (int32 [n]) of a 4-bit cache as bf16 pages k_out, v_out [Hk][n][64][128]
-    (rows at and behind a page's count are left as they are)."""
+def _unpack(name: str, cache: PagedKVCache, pages, k_out, v_out, stream):
     n = pages.shape[0]
     shp = (cache.n_kv_heads, n, PAGE, HEAD_DIM)
     dev = cache.tensors[0].get_device()
@@ -276,9 +312,20 @@ def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
     k, v = _at(k_out, torch.bfloat16, "k_out", shp, dev), _at(v_out, torch.bfloat16, "v_out", shp, dev)
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
-            return paged_kv_unpack_q4(cache, pages, k_out, v_out, stream)
+            return _unpack(name, cache, pages, k_out, v_out, stream)
     st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    check("paged_kv_unpack_q4", load().paged_kv_unpack_q4(cache.handle, at, n, k, v, st))
+    check(name, getattr(load(), name)(cache.handle, at, n, k, v, st))
+
+
+def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
+    """The listed physical pages (int32 [n]) of a 4-bit cache as bf16 pages k_out, v_out [Hk][n][64][128]
+    (rows at and behind a page's count are left as they are)."""
+    _unpack("paged_kv_unpack_q4", cache, pages, k_out, v_out, stream)
+
+
+def paged_kv_unpack_q8(cache: PagedKVCacheQ8, pages, k_out, v_out, stream=None):
+    """paged_kv_unpack_q4 for an 8-bit cache."""
+    _unpack("paged_kv_unpack_q8", cache, pages, k_out, v_out, stream)
 
 
 def paged_kv_append(cache: PagedKVCache, phys_page, tok_in_page, k_new, v_new, stream=None):

@@ -40,6 +40,13 @@ class SpkvDescQ4(ctypes.Structure):
                 ("ksum", _vp), ("page_cnt", _vp), ("max_units", ctypes.c_int32), ("ksum_bf16", ctypes.c_int32)]
 
 
+class SpkvDescQ8(ctypes.Structure):
+    _fields_ = [("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_tokens", ctypes.c_int32), ("subblock", ctypes.c_int32),
+                ("n_phys_pages", ctypes.c_int64), ("kv_pool", _vp), ("ksum", _vp), ("page_cnt", _vp),
+                ("max_units", ctypes.c_int32), ("ksum_bf16", ctypes.c_int32)]
+
+
 # spkv_rope: cos_sin, n_pos, n_axes, pair_axis, pos (packing takes a fifth of building a ctypes.Structure)
 ROPE = struct.Struct("@PqiPP")
 
@@ -52,6 +59,8 @@ SIGNATURES = {
     "paged_kv_append_rope": ([_vp, _vp, _i64, _vp, _i64, _i32, _i32, _vp, _vp, _vp, _i32, _vp, _vp,
                               _i64, _i32, _vp, _vp], _i32),
     "paged_kv_unpack_q4": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
+    "paged_kv_create_q8": ([ctypes.POINTER(SpkvDescQ8), _vp, ctypes.POINTER(_vp)], _i32),
+    "paged_kv_unpack_q8": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
     "score_blocks": ([_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
     "decode_append_score": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
     "select_topk": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp], _i32),

@@ -104,11 +104,11 @@ void fill_common(AttnParams& p, spkv_cache_t c, const void* q, int B, int Hq, fl
 
 // The selected-pages attention in the handle's format; grid bounds the persistent bf16 kernel's CTAs.
 int launch_sparse(spkv_cache_t c, const AttnParams& p, int grid, void* stream) {
-  if (c->pool4) {
+  if (c->packed()) {
     // it numbers tokens, and all units' pages and a few places for each unit, in 32 bits, and writes two values of a
     // row together
     if (!on_device(c) || !aligned(p.out, 8) || p.np_max > (1 << 25) || int64_t(p.B) * p.Hk * (int64_t(p.sel_stride) + 8) >= (int64_t(1) << 31)) return SPKV_EINVAL;
-    return status_of(spkv::launch_attn_q4(c, p, as_stream(stream)));
+    return status_of(c->pool4 ? spkv::launch_attn_q4(c, p, as_stream(stream)) : spkv::launch_attn_q8(c, p, as_stream(stream)));
   }
   return status_of(spkv::launch_attn(c, p, false, grid, as_stream(stream)));
 }
@@ -116,10 +116,12 @@ int launch_sparse(spkv_cache_t c, const AttnParams& p, int grid, void* stream) {
 }  // namespace
 
 namespace spkv {
-cudaError_t init_kernel_attributes(bool q4) {
+cudaError_t init_kernel_attributes(const spkv_cache* c) {
   cudaError_t e;
-  if (q4) {
+  if (c->pool4) {
     if ((e = attn_q4_init_attributes()) != cudaSuccess) return e;
+  } else if (c->pool8) {
+    if ((e = attn_q8_init_attributes()) != cudaSuccess) return e;
   } else {
     if ((e = attn_init_attributes()) != cudaSuccess) return e;
     if ((e = prefill_init_attributes()) != cudaSuccess) return e;
@@ -146,7 +148,7 @@ const char* spkv_status_string(int s) {
   }
 }
 
-// What both cache formats check of a description besides its pools.
+// What all cache formats check of a description besides its pools.
 static int check_desc(const spkv_desc& d) {
   if (d.head_dim != 128 || d.page_tokens != 64 || d.subblock != 16) return SPKV_EUNSUPPORTED;
   if (d.n_kv_heads <= 0 || d.n_phys_pages <= 0 || d.max_units < 0 || d.max_units > 4096) return SPKV_EINVAL;
@@ -156,9 +158,9 @@ static int check_desc(const spkv_desc& d) {
   return SPKV_OK;
 }
 
-// Allocates and initialises the handle of a checked description (4-bit: pool4 and the head scales).
-static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scale, const float* v_scale, void* stream,
-                         spkv_cache_t* out) {
+// Allocates and initialises the handle of a checked description (4-bit: pool4 and the head scales; 8-bit: pool8).
+static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scale, const float* v_scale, uint8_t* pool8,
+                         void* stream, spkv_cache_t* out) {
   const int64_t n_ph = int64_t(d.n_kv_heads) * d.n_phys_pages;
   if (n_ph >= (int64_t(1) << 31)) return SPKV_EUNSUPPORTED;
 
@@ -168,6 +170,7 @@ static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scal
   c->pool4 = pool4;
   c->k_scale = k_scale;
   c->v_scale = v_scale;
+  c->pool8 = pool8;
   c->max_units = d.max_units > 0 ? d.max_units : kMaxUnitsDefault;
   if (cudaGetDevice(&c->device) != cudaSuccess ||
       cudaDeviceGetAttribute(&c->sm_count, cudaDevAttrMultiProcessorCount, c->device) != cudaSuccess) {
@@ -175,11 +178,11 @@ static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scal
     return SPKV_ECUDA;
   }
   c->attn_grid = c->sm_count;
-  if (spkv::init_kernel_attributes(pool4 != nullptr) != cudaSuccess) {
+  if (spkv::init_kernel_attributes(c) != cudaSuccess) {
     delete c;
     return SPKV_ECUDA;
   }
-  if (!pool4 && (!encode_pool(&c->tmap_k, d.k_pool, n_ph) || !encode_pool(&c->tmap_v, d.v_pool, n_ph))) {
+  if (!c->packed() && (!encode_pool(&c->tmap_k, d.k_pool, n_ph) || !encode_pool(&c->tmap_v, d.v_pool, n_ph))) {
     delete c;
     return SPKV_ECUDA;
   }
@@ -196,9 +199,10 @@ static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scal
     return SPKV_ENOMEM;
   }
   cudaStream_t st = as_stream(stream);
+  const auto sums = pool4 ? spkv::launch_summary_build_q4 : pool8 ? spkv::launch_summary_build_q8 : spkv::launch_summary_build;
   if (cudaMemsetAsync(c->dev_err, 0, sizeof(uint32_t), st) != cudaSuccess ||
       cudaMemsetAsync(c->ws_cnt, 0, sizeof(int32_t) * (2 * c->max_units + 2), st) != cudaSuccess ||
-      (d.ksum && (pool4 ? spkv::launch_summary_build_q4(c, st) : spkv::launch_summary_build(c, st)) != cudaSuccess)) {
+      (d.ksum && sums(c, st) != cudaSuccess)) {
     paged_kv_destroy(c);
     return SPKV_ECUDA;
   }
@@ -213,7 +217,7 @@ int paged_kv_create(const spkv_desc* desc, void* stream, spkv_cache_t* out) {
   if (st != SPKV_OK) return st;
   if (!desc->ksum != !desc->page_cnt) return SPKV_EINVAL;
   if (!desc->k_pool || !desc->v_pool || !aligned(desc->k_pool, 16) || !aligned(desc->v_pool, 16)) return SPKV_EINVAL;
-  return create_handle(*desc, nullptr, nullptr, nullptr, stream, out);
+  return create_handle(*desc, nullptr, nullptr, nullptr, nullptr, stream, out);
 }
 
 int paged_kv_create_q4(const spkv_desc_q4* desc, void* stream, spkv_cache_t* out) {
@@ -232,7 +236,26 @@ int paged_kv_create_q4(const spkv_desc_q4* desc, void* stream, spkv_cache_t* out
   const int st = check_desc(d);
   if (st != SPKV_OK) return st;
   if (!desc->kv_pool || !aligned(desc->kv_pool, 16) || !desc->k_scale || !desc->v_scale) return SPKV_EINVAL;
-  return create_handle(d, static_cast<uint8_t*>(desc->kv_pool), desc->k_scale, desc->v_scale, stream, out);
+  return create_handle(d, static_cast<uint8_t*>(desc->kv_pool), desc->k_scale, desc->v_scale, nullptr, stream, out);
+}
+
+int paged_kv_create_q8(const spkv_desc_q8* desc, void* stream, spkv_cache_t* out) {
+  if (!desc || !out) return SPKV_EINVAL;
+  *out = nullptr;
+  spkv_desc d = {};
+  d.n_kv_heads = desc->n_kv_heads;
+  d.head_dim = desc->head_dim;
+  d.page_tokens = desc->page_tokens;
+  d.subblock = desc->subblock;
+  d.n_phys_pages = desc->n_phys_pages;
+  d.ksum = desc->ksum;
+  d.page_cnt = desc->page_cnt;
+  d.max_units = desc->max_units;
+  d.ksum_bf16 = desc->ksum_bf16;
+  const int st = check_desc(d);
+  if (st != SPKV_OK) return st;
+  if (!desc->kv_pool || !aligned(desc->kv_pool, 16)) return SPKV_EINVAL;
+  return create_handle(d, nullptr, nullptr, nullptr, static_cast<uint8_t*>(desc->kv_pool), stream, out);
 }
 
 int paged_kv_destroy(spkv_cache_t c) {
@@ -257,7 +280,7 @@ int spkv_set_wait_limit(spkv_cache_t c, uint64_t ns) {
 int paged_kv_append(spkv_cache_t c, const int32_t* phys_page, const int32_t* tok_in_page, const void* k_new,
                     const void* v_new, int n_rows, void* stream) {
   if (!c || !c->d.ksum || n_rows < 0) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (n_rows == 0) return SPKV_OK;
   if (!phys_page || !tok_in_page || !k_new || !v_new || !aligned(k_new, 4) || !aligned(v_new, 4)) return SPKV_EINVAL;
   return status_of(spkv::launch_append(c, phys_page, tok_in_page, k_new, v_new, n_rows, as_stream(stream)));
@@ -313,7 +336,7 @@ int paged_kv_append_rope(spkv_cache_t c, const void* k_new, int64_t k_stride, co
   p.seq_len = seq_len;
   p.page_table = page_table;
   p.np_max = np_max;
-  p.pool = c->pool4 ? c->pool4 : static_cast<uint8_t*>(c->d.k_pool);
+  p.pool = c->pool4 ? c->pool4 : c->pool8 ? c->pool8 : static_cast<uint8_t*>(c->d.k_pool);
   p.v_pool = static_cast<uint8_t*>(c->d.v_pool);
   p.k_scale = c->k_scale;
   p.v_scale = c->v_scale;
@@ -322,15 +345,27 @@ int paged_kv_append_rope(spkv_cache_t c, const void* k_new, int64_t k_stride, co
   p.page_cnt = c->d.page_cnt;
   p.n_phys = c->d.n_phys_pages;
   p.err = c->dev_err;
-  return status_of(spkv::launch_append_rope(c, p, as_stream(stream)));
+  return status_of(c->pool8 ? spkv::launch_append_q8(c, p, as_stream(stream)) : spkv::launch_append_rope(c, p, as_stream(stream)));
+}
+
+// Pages of a packed cache back as bf16; its: the handle is of the call's format.
+static int unpack(spkv_cache_t c, bool its, decltype(spkv::launch_unpack_q4)* launch, const int32_t* pages, int n_pages,
+                  void* k_out, void* v_out, void* stream) {
+  if (n_pages < 0) return SPKV_EINVAL;
+  if (!its || c->d.n_kv_heads > 65535) return SPKV_EUNSUPPORTED;
+  if (n_pages == 0) return SPKV_OK;
+  if (!pages || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || !on_device(c)) return SPKV_EINVAL;
+  return status_of(launch(c, pages, n_pages, k_out, v_out, as_stream(stream)));
 }
 
 int paged_kv_unpack_q4(spkv_cache_t c, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream) {
-  if (!c || n_pages < 0) return SPKV_EINVAL;
-  if (!c->pool4 || c->d.n_kv_heads > 65535) return SPKV_EUNSUPPORTED;
-  if (n_pages == 0) return SPKV_OK;
-  if (!pages || !k_out || !v_out || !aligned(k_out, 16) || !aligned(v_out, 16) || !on_device(c)) return SPKV_EINVAL;
-  return status_of(spkv::launch_unpack_q4(c, pages, n_pages, k_out, v_out, as_stream(stream)));
+  if (!c) return SPKV_EINVAL;
+  return unpack(c, c->pool4 != nullptr, spkv::launch_unpack_q4, pages, n_pages, k_out, v_out, stream);
+}
+
+int paged_kv_unpack_q8(spkv_cache_t c, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream) {
+  if (!c) return SPKV_EINVAL;
+  return unpack(c, c->pool8 != nullptr, spkv::launch_unpack_q8, pages, n_pages, k_out, v_out, stream);
 }
 
 int score_blocks(spkv_cache_t c, const void* q, int B, int Hq, const int32_t* page_table, int np_max,
@@ -347,7 +382,7 @@ int decode_append_score(spkv_cache_t c, const void* k_new, const void* v_new, co
                         const int32_t* page_table, int np_max, const int32_t* seq_len, float* scores, void* stream) {
   int st = check_group(c, B, Hq);
   if (st != SPKV_OK) return st;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (!c->d.ksum) return SPKV_EINVAL;
   if (B == 0) return SPKV_OK;
   if (!q || !page_table || !seq_len || !scores || np_max <= 0 || !aligned(q, 8)) return SPKV_EINVAL;
@@ -420,7 +455,7 @@ int lazy_rope_decode_attn(spkv_cache_t c, const void* q, int B, int Hq, const in
                           float theta, float* out, float* lse, void* stream) {
   int st = check_group(c, B, Hq);
   if (st != SPKV_OK) return st;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (B == 0) return SPKV_OK;
   if (!q || !qpos || !meta || !n_pages || !doc_pos || !out || !lse || np_max <= 0 || max_docs <= 0 ||
       !aligned(q, 16))
@@ -452,7 +487,7 @@ static int rope_prefill(spkv_cache_t c, const void* q, int B, int T, int Hq, con
                         const int32_t* page_start, const int32_t* doc_pos, int max_docs, float theta, float* out,
                         float* lse, void* stream) {
   if (!c || B < 0 || T < 0 || Hq <= 0) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   if (Hq / Hk > kMaxGroup) return SPKV_EUNSUPPORTED;
@@ -513,7 +548,7 @@ int lazy_alibi_prefill_attn(spkv_cache_t c, const void* q, int B, int T, int Hq,
                             const int32_t* page_start, const int32_t* doc_pos, int max_docs, const float* slopes,
                             float* out, float* lse, void* stream) {
   if (!c || B < 0 || T < 0 || Hq <= 0) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   if (Hq / Hk > kMaxGroup) return SPKV_EUNSUPPORTED;
@@ -551,7 +586,7 @@ int lazy_alibi_prefill_attn(spkv_cache_t c, const void* q, int B, int T, int Hq,
 static int column_scores(spkv_cache_t c, const void* q, const float* lse_in, int B, int alpha, int Hq,
                   const int32_t* page_table, int np_max, const int32_t* seq_len, float* scores, void* stream) {
   if (!c || B < 0 || Hq <= 0 || alpha < 0) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   if (alpha > kMaxColumnRows || Hq / Hk > kMaxGroup) return SPKV_EUNSUPPORTED;
@@ -663,7 +698,7 @@ static int retrieve_common(spkv_cache_t c, const void* k_host, const void* v_hos
                            const int32_t* missing, const int32_t* n_missing, const int32_t* victims, int32_t* slot,
                            const int32_t* n_sel, int sel_stride, int n_slots, void* stream) {
   if (!c || B < 0) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   if (B == 0) return SPKV_OK;
   if (!k_host || !v_host || (!page_table && !pd) || !missing || !n_missing || !victims || !slot || !n_sel)
     return SPKV_EINVAL;

@@ -55,7 +55,7 @@ int lazy_docs_plan_create(spkv_cache_t c, int B, int Hq, const int32_t* req_docs
   if (!out) return SPKV_EINVAL;
   *out = nullptr;
   if (!c || B <= 0 || Hq <= 0 || max_docs <= 0 || n_docs <= 0 || !req_docs || !doc_first) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;   // bf16 pools only
+  if (c->packed()) return SPKV_EUNSUPPORTED;   // bf16 pools only
   const int Hk = c->d.n_kv_heads;
   if (Hq % Hk != 0) return SPKV_EINVAL;
   const int G = Hq / Hk;
@@ -145,7 +145,7 @@ int lazy_rope_decode_attn_docs(spkv_cache_t c, spkv_doc_plan_t pl, const void* q
                                const uint32_t* doc_pages, const int32_t* doc_first, const int32_t* doc_pos,
                                float theta, float* out, float* lse, void* stream) {
   if (!c || !pl || !q || !qpos || !doc_pages || !doc_first || !doc_pos || !out || !lse) return SPKV_EINVAL;
-  if (c->pool4) return SPKV_EUNSUPPORTED;
+  if (c->packed()) return SPKV_EUNSUPPORTED;
   if (pl->Hk != c->d.n_kv_heads || (reinterpret_cast<uintptr_t>(q) % 16) != 0) return SPKV_EINVAL;
   if (!(theta > 1.0f) || !std::isfinite(theta)) return SPKV_EINVAL;
   spkv::AttnParams p;

@@ -32,6 +32,8 @@ struct spkv_cache {
   uint8_t* pool4 = nullptr;      // 4-bit handle: its pool [Hk][n_phys][9216] (no tensor maps, d.k_pool unused)
   const float* k_scale = nullptr;   // 4-bit handle: [Hk]
   const float* v_scale = nullptr;
+  uint8_t* pool8 = nullptr;      // 8-bit handle: its pool [Hk][n_phys][16416]
+  bool packed() const { return pool4 || pool8; }   // no bf16 pools
 };
 
 namespace spkv {
@@ -65,10 +67,10 @@ cudaError_t launch_pdl(void (*k)(KArgs...), dim3 grid, dim3 block, size_t smem, 
   return cudaLaunchKernelEx(&cfg, k, std::forward<Args>(args)...);
 }
 
-// Sets the dynamic shared-memory limits of the kernels that a handle's calls launch, a 4-bit one's (q4) or a
-// bf16 one's, at its creation (which loads them), so that no launch path calls cudaFuncSetAttribute and every
-// call can be captured in a CUDA graph.
-cudaError_t init_kernel_attributes(bool q4);
+// Sets the dynamic shared-memory limits of the kernels that the handle's calls launch, its own format's, at its
+// creation (which loads them), so that no launch path calls cudaFuncSetAttribute and every call can be captured
+// in a CUDA graph.
+cudaError_t init_kernel_attributes(const spkv_cache* c);
 
 // Parameters of the split-K attention kernel (sparse and lazy forms).
 struct AttnParams {
@@ -170,7 +172,14 @@ struct AttnQ4Params {
   int parts, part_pages;  // CTAs a unit where CTAs take units, at most; pages of a part, at least
 };
 
-// Parameters of the rotating append (either cache format).
+// The same over an 8-bit pool.
+struct AttnQ8Params {
+  AttnParams a;
+  const uint8_t* pool;
+  int parts, part_pages;
+};
+
+// Parameters of the rotating append (any cache format).
 struct AppendRopeParams {
   const uint16_t* k_new;         // bf16 rows, k_stride elements apart, [Hk][128] each
   const uint16_t* v_new;
@@ -189,7 +198,7 @@ struct AppendRopeParams {
   uint64_t pair_axis[2];         // two bits a pair
   int quads;                     // pairs 4l .. 4l + 3 have one axis, for every l
   int window;                    // rows per CTA (set by the launch)
-  uint8_t* pool;                 // key pool (bf16) or the 4-bit pool
+  uint8_t* pool;                 // key pool (bf16) or the 4-bit or 8-bit pool
   uint8_t* v_pool;               // bf16 form
   const float* k_scale;
   const float* v_scale;
@@ -207,6 +216,12 @@ cudaError_t launch_unpack_q4(const spkv_cache* c, const int32_t* pages, int n_pa
                              cudaStream_t st);
 cudaError_t launch_attn_q4(const spkv_cache* c, const AttnParams& a, cudaStream_t st);
 cudaError_t attn_q4_init_attributes();
+cudaError_t launch_summary_build_q8(const spkv_cache* c, cudaStream_t st);
+cudaError_t launch_append_q8(const spkv_cache* c, AppendRopeParams& p, cudaStream_t st);
+cudaError_t launch_unpack_q8(const spkv_cache* c, const int32_t* pages, int n_pages, void* k_out, void* v_out,
+                             cudaStream_t st);
+cudaError_t launch_attn_q8(const spkv_cache* c, const AttnParams& a, cudaStream_t st);
+cudaError_t attn_q8_init_attributes();
 cudaError_t launch_append(const spkv_cache* c, const int32_t* phys, const int32_t* tok, const void* k_new,
                           const void* v_new, int n_rows, cudaStream_t st);
 // The fused decode append's pointers (k_new, v_new: bf16 [B][Hk][128] as 32-bit words).
