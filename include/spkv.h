@@ -25,6 +25,8 @@
  *                        the three sparse_decode_attn calls work on it
  *   paged_kv_unpack_q4   pages of a 4-bit cache back as bf16 pages
  *   paged_kv_create_q8, paged_kv_unpack_q8  the same for a cache held in 8 bits, one scale for 16 tokens of a head
+ *   beam_select          the best continuations of a request's beams over the vocabulary
+ *   beam_reorder         the beams' pages follow their parents: tables permuted, part-filled pages copied
  *   score_blocks_dir, sparse_decode_attn_dir, retrieve_pages_dir  the same calls through a
  *                        two-level page directory (spkv_pagemap_* manages one)
  *
@@ -82,6 +84,7 @@ enum spkv_status {
 #define SPKV_DEVERR_CAPACITY 16u    /* more missing pages than evictable slots */
 #define SPKV_DEVERR_TIMEOUT 32u     /* a bounded intra-CTA wait gave up (reported as SPKV_ETIMEOUT) */
 #define SPKV_DEVERR_POS 64u         /* rotary position outside the table of cos and sin */
+#define SPKV_DEVERR_BEAM 128u       /* a beam's logits or score NaN or +infinity; parents that are no beams, beams of unlike lengths */
 
 typedef struct spkv_cache* spkv_cache_t; /* opaque, library-owned */
 
@@ -265,6 +268,50 @@ int paged_kv_create_q8(const spkv_desc_q8* desc, void* stream, spkv_cache_t* out
 
 /* paged_kv_unpack_q4 for an 8-bit cache; the values are exact. */
 int paged_kv_unpack_q8(spkv_cache_t cache, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream);
+
+/* Beam search over a paged cache: a decode step of B requests with W beams each is a step of B * W sequences (row
+ * b * W + w of every tensor is beam w of request b), then beam_select on its logits and beam_reorder. */
+
+enum spkv_dtype { SPKV_F32 = 0, SPKV_BF16 = 1, SPKV_F16 = 2 };
+
+/* Workspace of beam_select for up to max_rows = B * W beams and max_vocab tokens (max_rows <= 65536, max_vocab <= 2^24, else
+ * SPKV_EUNSUPPORTED), on the cache's device, which has to be the current one; about 0.13 bytes for each beam and token.  It
+ * is prepared on `stream`.  A plan serves one stream at a time. */
+typedef struct spkv_beam_plan* spkv_beam_plan_t;
+int beam_plan_create(spkv_cache_t cache, int max_rows, int max_vocab, void* stream, spkv_beam_plan_t* out);
+int beam_plan_destroy(spkv_beam_plan_t plan);
+
+/* The K best continuations of each request:
+ *   score[w][v] = cum[b][w] + (logits[b W + w][v] - log sum_u exp(logits[b W + w][u]))
+ * over beams w and tokens v, best first; of equal scores the lower beam, then the lower token goes first.  Sums are formed in
+ * fp32 over 4 KiB of a row, then in 64 bits, as are scores.
+ *   logits  : device, rows row_stride elements apart, each [V] of `type`; aligned to its elements
+ *   cum     : device fp32 [B][W], the beams' scores so far; -infinity: a beam that has ended or does not exist yet (its
+ *             logits are not read, it has no candidates)
+ *   tokens, parents, scores : device int32, int32, fp32 [B][K]; where there are fewer than K candidates -1, -1, -infinity
+ * A logit of -infinity is no candidate (masks may use it, or their type's lowest value).  A beam whose logits or score hold a
+ * NaN or +infinity has no candidates (SPKV_DEVERR_BEAM).  K may be larger than W, for callers that take the ended ones out;
+ * W <= 64, K <= 128 (else SPKV_EUNSUPPORTED). */
+int beam_select(spkv_cache_t cache, spkv_beam_plan_t plan, const void* logits, int type, int64_t row_stride, int B, int W,
+                int V, const float* cum, int K, int32_t* tokens, int32_t* parents, float* scores, void* stream);
+
+/* The beams of each request continue parents[b][w] of them (-1: beam w stops; its complete pages stay as they are).  With
+ * L = seq_len[b W + w] tokens in each of the request's beams:
+ *   columns j < L / 64 of the tables (complete pages): page_table[b W + w][j] = its parent's; the pages are then shared
+ *   column L / 64, if L % 64 > 0 (the page that the next token goes to, of which each beam must have its own): a parent's
+ *     child (the beam itself if it is one, else the lowest) keeps the parent's page; every other beam, in order, gets the page
+ *     of a beam without children, in order, and the parent's rows, sums and page_cnt are copied there
+ *   columns behind: as they are
+ * Before the first step, with the prompt in beam 0's pages and a page of its own in column L / 64 of every beam, parents of 0
+ * make all beams continue it.  Pages that no table names any more are the caller's to find (complete pages only: none is lost
+ * from column L / 64).  Any cache format; handles without summaries or page_cnt have whole pages copied.
+ *   parents    : device int32 [B][W];  seq_len: device int32 [B W]
+ *   page_table : device int32 [B W][np_max], changed in place
+ * A request with a parent outside [-1, W) or beams of different lengths is left as it is (SPKV_DEVERR_BEAM), one with column
+ * L / 64 outside the table too (SPKV_DEVERR_PAGE_ID); a copy from or to a page outside the pool is left out
+ * (SPKV_DEVERR_PHYS).  W <= 64 (else SPKV_EUNSUPPORTED), B * W * n_kv_heads <= max_units. */
+int beam_reorder(spkv_cache_t cache, const int32_t* parents, int B, int W, int32_t* page_table, int np_max,
+                 const int32_t* seq_len, void* stream);
 
 /* Block scores, [NOSA] "Method 1", block-wise implementation (two-stage pooling: mean over
  * each 16-token sub-block, max over the 4 sub-blocks of the page) and dual selection

@@ -31,6 +31,12 @@ With the cache held in 4 bits, and the rotary positions applied where rows are a
 and in 8 bits, with a scale for each sub-block of 16 tokens that the append finds by itself:
 
     cache = paged_kv_create_q8(kv_pool, ksum, page_cnt)       # then the same calls, and paged_kv_unpack_q8
+
+With W beams a request, row b W + w of every tensor being beam w of request b, behind a decode step:
+
+    plan = BeamPlan(cache, B * W, V)
+    beam_select(cache, plan, logits, cum, tokens, parents, scores)
+    beam_reorder(cache, parents, page_table, seq_len)         # any cache; tables in place, part-filled pages copied
 """
 from __future__ import annotations
 
@@ -51,6 +57,7 @@ __all__ = ["PagedKVCache", "paged_kv_create", "paged_kv_append", "score_blocks",
            "PageMap", "score_blocks_dir", "sparse_decode_attn_dir", "retrieve_pages_dir", "DocPlan",
            "lazy_rope_decode_attn_docs", "PagedKVCacheQ4", "paged_kv_create_q4", "paged_kv_append_rope",
            "paged_kv_unpack_q4", "PagedKVCacheQ8", "paged_kv_create_q8", "paged_kv_unpack_q8",
+           "BeamPlan", "beam_select", "beam_reorder",
            "load"]
 
 HEAD_DIM, PAGE, SUBBLOCK = 128, 64, 16
@@ -326,6 +333,81 @@ def paged_kv_unpack_q4(cache: PagedKVCacheQ4, pages, k_out, v_out, stream=None):
 def paged_kv_unpack_q8(cache: PagedKVCacheQ8, pages, k_out, v_out, stream=None):
     """paged_kv_unpack_q4 for an 8-bit cache."""
     _unpack("paged_kv_unpack_q8", cache, pages, k_out, v_out, stream)
+
+
+class BeamPlan:
+    """Workspace of ``beam_select`` for up to ``max_rows`` beams (of all requests together) and ``max_vocab`` tokens."""
+
+    def __init__(self, cache: PagedKVCache, max_rows: int, max_vocab: int, stream=None):
+        self.handle = None
+        h = ctypes.c_void_p()
+        with torch.cuda.device(cache.tensors[0].device):
+            check("beam_plan_create", load().beam_plan_create(cache.handle, int(max_rows), int(max_vocab), _stream(stream),
+                                                              ctypes.byref(h)))
+        self.handle, self.max_rows, self.max_vocab = h, int(max_rows), int(max_vocab)
+
+    def close(self):
+        if self.handle:
+            torch.cuda.synchronize()
+            check("beam_plan_destroy", load().beam_plan_destroy(self.handle))
+            self.handle = None
+
+    def __del__(self):
+        try:
+            if self.handle:
+                load().beam_plan_destroy(self.handle)
+                self.handle = None
+        except Exception:
+            pass
+
+
+_LOGITS = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+
+
+def beam_select(cache: PagedKVCache, plan: BeamPlan, logits, cum, tokens, parents, scores, stream=None):
+    """The K best continuations of each request's W beams: logits fp32, bf16 or fp16 [B][W][V] (rows may lie apart, evenly),
+    cum fp32 [B][W] the beams' scores so far (-inf: none); tokens, parents int32 and scores fp32 [B][K], best first, -1, -1,
+    -inf where there are fewer."""
+    if not isinstance(logits, torch.Tensor):
+        raise TypeError("logits: expected a torch.Tensor")
+    kind = _LOGITS.get(logits.dtype)
+    if kind is None:
+        raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
+    dev = cache.tensors[0].get_device()
+    if logits.get_device() != dev or dev < 0:
+        raise ValueError("logits: must be a CUDA tensor on the cache's device")
+    if logits.dim() != 3:
+        raise ValueError("logits: expected [B][W][V]")
+    B, W, V = logits.shape
+    sb, sw, one = logits.stride()
+    row = sw if W > 1 else sb if B > 1 else V
+    if (one != 1 and V > 1) or (B > 1 and W > 1 and sb != W * sw):
+        raise ValueError("logits: rows must be contiguous and evenly apart")
+    K = tokens.shape[1] if tokens.dim() == 2 else 0
+    c = _at(cum, torch.float32, "cum", (B, W), dev)
+    t, p = _at(tokens, torch.int32, "tokens", (B, K), dev), _at(parents, torch.int32, "parents", (B, K), dev)
+    s = _at(scores, torch.float32, "scores", (B, K), dev)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return beam_select(cache, plan, logits, cum, tokens, parents, scores, stream)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    check("beam_select", load().beam_select(cache.handle, plan.handle, logits.data_ptr(), kind, row, B, W, V, c, K, t, p, s, st))
+
+
+def beam_reorder(cache: PagedKVCache, parents, page_table, seq_len, stream=None):
+    """Beam w of request b continues parents[b][w] (int32 [B][W], -1: it stops): its row b W + w of page_table (int32
+    [B W][np_max]) gets the parent's complete pages, and where the parent's last page is part-filled and another child keeps
+    it, a page of its own with the parent's rows.  seq_len int32 [B W]: the tokens in the beams, alike in a request."""
+    B, W = parents.shape
+    np_max = page_table.shape[1]
+    dev = cache.tensors[0].get_device()
+    p = _at(parents, torch.int32, "parents", (B, W), dev)
+    t, n = _at(page_table, torch.int32, "page_table", (B * W, np_max), dev), _at(seq_len, torch.int32, "seq_len", (B * W,), dev)
+    if torch._C._cuda_getDevice() != dev:
+        with torch.cuda.device(dev):
+            return beam_reorder(cache, parents, page_table, seq_len, stream)
+    st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
+    check("beam_reorder", load().beam_reorder(cache.handle, p, B, W, t, np_max, n, st))
 
 
 def paged_kv_append(cache: PagedKVCache, phys_page, tok_in_page, k_new, v_new, stream=None):

@@ -14,7 +14,7 @@ SO_PATH = os.path.join(_HERE, "libspkv.so")
 
 SPKV_OK, SPKV_EINVAL, SPKV_ENOMEM, SPKV_ECUDA, SPKV_EDEVICE, SPKV_ETIMEOUT, SPKV_EUNSUPPORTED = \
     0, -1, -2, -3, -4, -5, -6
-DEVERR = {"PAGE_ID": 1, "PHYS": 2, "SLOT": 4, "ORDER": 8, "CAPACITY": 16, "TIMEOUT": 32, "POS": 64}
+DEVERR = {"PAGE_ID": 1, "PHYS": 2, "SLOT": 4, "ORDER": 8, "CAPACITY": 16, "TIMEOUT": 32, "POS": 64, "BEAM": 128}
 
 # Every entry point declared in include/spkv.h, with its ctypes signature.
 _vp, _i32, _i64, _u32, _f32 = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_uint32, ctypes.c_float
@@ -61,6 +61,10 @@ SIGNATURES = {
     "paged_kv_unpack_q4": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
     "paged_kv_create_q8": ([ctypes.POINTER(SpkvDescQ8), _vp, ctypes.POINTER(_vp)], _i32),
     "paged_kv_unpack_q8": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
+    "beam_plan_create": ([_vp, _i32, _i32, _vp, ctypes.POINTER(_vp)], _i32),
+    "beam_plan_destroy": ([_vp], _i32),
+    "beam_select": ([_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
+    "beam_reorder": ([_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp], _i32),
     "score_blocks": ([_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
     "decode_append_score": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp, _vp], _i32),
     "select_topk": ([_vp, _vp, _vp, _vp, _i32, _i32, _vp, _i32, _i32, _vp, _vp, _vp], _i32),

@@ -15,7 +15,7 @@ CSRC = os.path.join(HERE, "csrc")
 SO = os.path.join(HERE, "libspkv.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "attn.cu", "score.cu", "select.cu", "summary.cu", "resid.cu", "fused.cu", "prefill.cu", "colscore.cu", "retrieve.cu", "noalloc.cu", "pagemap.cu", "docplan.cu",
-           "q4.cu", "append_rope.cu", "attn_q4.cu", "q8.cu", "append_q8.cu", "attn_q8.cu"]
+           "q4.cu", "append_rope.cu", "attn_q4.cu", "q8.cu", "append_q8.cu", "attn_q8.cu", "beam.cu"]
 
 
 def _nvcc() -> str:

@@ -192,7 +192,8 @@ static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scal
             cudaMalloc(&c->ws_m, sizeof(float) * 16 * c->ws_slots) == cudaSuccess &&
             cudaMalloc(&c->ws_l, sizeof(float) * 16 * c->ws_slots) == cudaSuccess &&
             cudaMalloc(&c->ws_o, sizeof(float) * 16 * 128 * c->ws_slots) == cudaSuccess &&
-            cudaMalloc(&c->ws_cnt, sizeof(int32_t) * (2 * c->max_units + 2)) == cudaSuccess;
+            cudaMalloc(&c->ws_cnt, sizeof(int32_t) * (2 * c->max_units + 2)) == cudaSuccess &&
+            cudaMalloc(&c->beam_cnt, sizeof(int32_t) * c->max_units) == cudaSuccess;
   if (!ok) {
     cudaGetLastError();
     paged_kv_destroy(c);
@@ -202,6 +203,7 @@ static int create_handle(const spkv_desc& d, uint8_t* pool4, const float* k_scal
   const auto sums = pool4 ? spkv::launch_summary_build_q4 : pool8 ? spkv::launch_summary_build_q8 : spkv::launch_summary_build;
   if (cudaMemsetAsync(c->dev_err, 0, sizeof(uint32_t), st) != cudaSuccess ||
       cudaMemsetAsync(c->ws_cnt, 0, sizeof(int32_t) * (2 * c->max_units + 2), st) != cudaSuccess ||
+      cudaMemsetAsync(c->beam_cnt, 0, sizeof(int32_t) * c->max_units, st) != cudaSuccess ||
       (d.ksum && sums(c, st) != cudaSuccess)) {
     paged_kv_destroy(c);
     return SPKV_ECUDA;
@@ -265,6 +267,7 @@ int paged_kv_destroy(spkv_cache_t c) {
   cudaFree(c->ws_l);
   cudaFree(c->ws_o);
   cudaFree(c->ws_cnt);
+  cudaFree(c->beam_cnt);
   delete c;
   return SPKV_OK;
 }

@@ -20,6 +20,7 @@ struct spkv_cache {
   float* ws_l = nullptr;         // split-K partial row sum   [slots][16]
   float* ws_o = nullptr;         // split-K partial outputs   [slots][16][128]
   int32_t* ws_cnt = nullptr;     // per unit (first segment, segments) [2 * max_units], then the chunk counter
+  int32_t* beam_cnt = nullptr;   // per request: CTAs of beam_reorder that have read its tables [max_units], 0 between calls
   int64_t ws_slots = 0;
   int32_t max_units = 0;
   int attn_grid = 0;             // CTAs of the split-K attention kernel (one per SM)
