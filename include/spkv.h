@@ -275,23 +275,23 @@ int paged_kv_unpack_q8(spkv_cache_t cache, const int32_t* pages, int n_pages, vo
 enum spkv_dtype { SPKV_F32 = 0, SPKV_BF16 = 1, SPKV_F16 = 2 };
 
 /* Workspace of beam_select for up to max_rows = B * W beams and max_vocab tokens (max_rows <= 65536, max_vocab <= 2^24, else
- * SPKV_EUNSUPPORTED), on the cache's device, which has to be the current one; about 0.13 bytes for each beam and token.  It
- * is prepared on `stream`.  A plan serves one stream at a time. */
+ * SPKV_EUNSUPPORTED), on the cache's device, which has to be the current one; about 0.13 bytes for each beam and token.  A plan
+ * serves one stream at a time. */
 typedef struct spkv_beam_plan* spkv_beam_plan_t;
-int beam_plan_create(spkv_cache_t cache, int max_rows, int max_vocab, void* stream, spkv_beam_plan_t* out);
+int beam_plan_create(spkv_cache_t cache, int max_rows, int max_vocab, spkv_beam_plan_t* out);
 int beam_plan_destroy(spkv_beam_plan_t plan);
 
 /* The K best continuations of each request:
  *   score[w][v] = cum[b][w] + (logits[b W + w][v] - log sum_u exp(logits[b W + w][u]))
  * over beams w and tokens v, best first; of equal scores the lower beam, then the lower token goes first.  Sums are formed in
- * fp32 over 4 KiB of a row, then in 64 bits, as are scores.
+ * fp32 over 4 KiB of a row, then in 48 bits, as are scores.
  *   logits  : device, rows row_stride elements apart, each [V] of `type`; aligned to its elements
  *   cum     : device fp32 [B][W], the beams' scores so far; -infinity: a beam that has ended or does not exist yet (its
  *             logits are not read, it has no candidates)
  *   tokens, parents, scores : device int32, int32, fp32 [B][K]; where there are fewer than K candidates -1, -1, -infinity
  * A logit of -infinity is no candidate (masks may use it, or their type's lowest value).  A beam whose logits or score hold a
  * NaN or +infinity has no candidates (SPKV_DEVERR_BEAM).  K may be larger than W, for callers that take the ended ones out;
- * W <= 64, K <= 128 (else SPKV_EUNSUPPORTED). */
+ * W <= 64, K <= 128, W rows of at most 2^27 bytes together (else SPKV_EUNSUPPORTED). */
 int beam_select(spkv_cache_t cache, spkv_beam_plan_t plan, const void* logits, int type, int64_t row_stride, int B, int W,
                 int V, const float* cum, int K, int32_t* tokens, int32_t* parents, float* scores, void* stream);
 

@@ -338,12 +338,11 @@ def paged_kv_unpack_q8(cache: PagedKVCacheQ8, pages, k_out, v_out, stream=None):
 class BeamPlan:
     """Workspace of ``beam_select`` for up to ``max_rows`` beams (of all requests together) and ``max_vocab`` tokens."""
 
-    def __init__(self, cache: PagedKVCache, max_rows: int, max_vocab: int, stream=None):
+    def __init__(self, cache: PagedKVCache, max_rows: int, max_vocab: int):
         self.handle = None
         h = ctypes.c_void_p()
         with torch.cuda.device(cache.tensors[0].device):
-            check("beam_plan_create", load().beam_plan_create(cache.handle, int(max_rows), int(max_vocab), _stream(stream),
-                                                              ctypes.byref(h)))
+            check("beam_plan_create", load().beam_plan_create(cache.handle, int(max_rows), int(max_vocab), ctypes.byref(h)))
         self.handle, self.max_rows, self.max_vocab = h, int(max_rows), int(max_vocab)
 
     def close(self):

@@ -61,7 +61,7 @@ SIGNATURES = {
     "paged_kv_unpack_q4": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
     "paged_kv_create_q8": ([ctypes.POINTER(SpkvDescQ8), _vp, ctypes.POINTER(_vp)], _i32),
     "paged_kv_unpack_q8": ([_vp, _vp, _i32, _vp, _vp, _vp], _i32),
-    "beam_plan_create": ([_vp, _i32, _i32, _vp, ctypes.POINTER(_vp)], _i32),
+    "beam_plan_create": ([_vp, _i32, _i32, ctypes.POINTER(_vp)], _i32),
     "beam_plan_destroy": ([_vp], _i32),
     "beam_select": ([_vp, _vp, _vp, _i32, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _vp, _vp], _i32),
     "beam_reorder": ([_vp, _vp, _i32, _i32, _vp, _i32, _vp, _vp], _i32),

@@ -4,12 +4,13 @@
 //   lse_w = log sum_v exp(x_wv),  score_wv = x_wv + (cum_w - lse_w),  the K best by score, then beam, then token.
 // The logits are read once.  A warp takes 4 KiB of a row (32 lines of 128 bytes, counted from the row's first element
 // wherever that lies in memory, so that rows with equal logits have equal sums): each line's maximum, the group's maximum
-// m and sum of exp(x - m).  The last CTA of a request to arrive has
-// then only maxima to look through: an element among the K best lies in a line whose maximum is among the K best of the
-// lines' (each line ahead of it holds an element ahead of it), and likewise a line in its group.  So it finds the K best
-// groups of all beams, of their lines the K best, and of those lines' elements, read again, the K best; of equal ones
-// the first each time, which is the order asked for, as groups, lines and elements are numbered by beam and token.
-// Sums are fp32 within 4 KiB, then 64 bits, as scores are: those of different beams may lie close together.
+// m and sum of exp(x - m).  A second kernel, a CTA a request, has then only maxima to look through: it searches for a score
+// that at least K of the groups' maxima reach, as then do the K best elements, for a score that K of those groups' lines
+// reach, and reads the elements of the lines that reach it again.  Where more are alike than its lists hold, it takes exactly
+// K groups, K of their lines and K elements, of equal ones the first each time (an element among the K best lies in a line
+// whose maximum is among the K best of the lines', as each line ahead of it holds an element ahead of it, and likewise a line
+// in its group; groups, lines and elements are numbered by beam and token).
+// Sums are fp32 within 4 KiB, then 48 bits, as scores are: those of different beams may lie close together.
 //
 // beam_reorder.  Complete pages are shared, so a child takes its parent's table entries; of the part-filled page a parent's
 // first child keeps the parent's own, and each other child gets the page of a beam without children, with the parent's rows
@@ -17,6 +18,7 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include <algorithm>
 #include <new>
 
 #include "common.cuh"
@@ -26,7 +28,6 @@ struct spkv_beam_plan {
   int max_rows = 0, max_vocab = 0, max_groups = 0;
   float* line_max = nullptr;     // [max_rows * max_groups][32]
   float2* group = nullptr;       // [max_rows * max_groups]: maximum, sum of exp(x - maximum)
-  int32_t* arrived = nullptr;    // [max_rows], 0 between calls
 };
 
 namespace spkv {
@@ -34,20 +35,21 @@ namespace {
 
 constexpr int kGroupBytes = 4096, kLineBytes = 128, kLines = kGroupBytes / kLineBytes;
 constexpr int kMaxBeams = 64, kMaxBest = 128;
-constexpr int kWarps = 8, kThreads = 32 * kWarps;
-constexpr int kKept = 4096;   // keys that are kept in shared memory; more are formed anew at each look
+constexpr int kWarps = 16, kThreads = 32 * kWarps;   // of the second kernel
+constexpr int kGroupThreads = 128, kCtasPerSm = 6, kStages = 2;   // of the first; groups of a warp in shared memory
+constexpr int kMaxGroups = 32768;   // of a request: as many keys as shared memory holds
 
 struct BeamParams {
   const uint8_t* logits;
   int64_t row_bytes;
-  int W, V, K, groups, ctas;     // groups: 4 KiB pieces of a row; ctas of a request
+  int W, V, K, groups;           // groups: 4 KiB pieces of a row
+  int rows;
   const float* cum;
   int32_t* tokens;
   int32_t* parents;
   float* scores;
   float* line_max;
   float2* group;
-  int32_t* arrived;
   uint32_t* err;
 };
 
@@ -59,7 +61,6 @@ struct Traits<float> {
   static __device__ __forceinline__ float top(uint4 v) {
     return fmaxf(fmaxf(__uint_as_float(v.x), __uint_as_float(v.y)), fmaxf(__uint_as_float(v.z), __uint_as_float(v.w)));
   }
-  static __device__ __forceinline__ float2 pair(uint32_t a, uint32_t b) { return make_float2(__uint_as_float(a), __uint_as_float(b)); }
   static __device__ __forceinline__ float one(const float* p) { return *p; }
 };
 template <>
@@ -87,43 +88,103 @@ struct Traits<__half> {
   static __device__ __forceinline__ float one(const __half* p) { return __half2float(*p); }
 };
 
-__device__ __forceinline__ float exp_of(float x, float m) {   // exp(x - m), x <= m
+__device__ __forceinline__ float ex2(float x) {
   float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"((x - m) * 1.4426950408889634f));
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
 }
+constexpr float kLog2e = 1.4426950408889634f;
+
+// s0 + s1 grow by 2^(x log2e - c) of each x: the product is exact within the fused addition, so a term is off by the
+// rounding of its own exponent only.
+__device__ __forceinline__ void add_exps(float& s0, float& s1, float x0, float x1, float c) {
+  float t0, t1;
+  fma_f32x2(t0, t1, x0, x1, kLog2e, kLog2e, -c, -c);
+  add_f32x2(s0, s1, ex2(t0), ex2(t1));
+}
 template <typename T>
-__device__ __forceinline__ float exps_of(uint4 v, float m) {
+__device__ __forceinline__ void add_exps(float& s0, float& s1, uint4 v, float c) {
   if constexpr (sizeof(T) == 4) {
-    return (exp_of(__uint_as_float(v.x), m) + exp_of(__uint_as_float(v.y), m)) +
-           (exp_of(__uint_as_float(v.z), m) + exp_of(__uint_as_float(v.w), m));
+    add_exps(s0, s1, __uint_as_float(v.x), __uint_as_float(v.y), c);
+    add_exps(s0, s1, __uint_as_float(v.z), __uint_as_float(v.w), c);
   } else {
-    const float2 a = Traits<T>::pair(v.x), b = Traits<T>::pair(v.y), c = Traits<T>::pair(v.z), d = Traits<T>::pair(v.w);
-    return ((exp_of(a.x, m) + exp_of(a.y, m)) + (exp_of(b.x, m) + exp_of(b.y, m))) +
-           ((exp_of(c.x, m) + exp_of(c.y, m)) + (exp_of(d.x, m) + exp_of(d.y, m)));
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float2 x = Traits<T>::pair(w[j]);
+      add_exps(s0, s1, x.x, x.y, c);
+    }
   }
 }
+// exp(x - m) for a maximum m of 2^126 or more, whose product with log2e may be no fp32 number: what is not m is too far away
+// to count.  NaN for NaN and for m = infinity, 0 for m = -infinity.
+__device__ __forceinline__ float far_exp(float x, float m) {
+  return x != x || m == CUDART_INF_F ? CUDART_NAN_F : x == m && m > -CUDART_INF_F ? 1.f : 0.f;
+}
+template <typename T>
+__device__ __forceinline__ float far_exps(uint4 v, float m) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  float s = 0.f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if constexpr (sizeof(T) == 4) {
+      s += far_exp(__uint_as_float(w[j]), m);
+    } else {
+      const float2 x = Traits<T>::pair(w[j]);
+      s += far_exp(x.x, m) + far_exp(x.y, m);
+    }
+  }
+  return s;
+}
 
-// Scores as integers of the same order; 0 for what is no candidate (-infinity, NaN).
+// Numbers of about 48 bits: hi is the nearest fp32 number, lo the rest.  (This card's 64-bit units are few: a warp's
+// addition keeps an SM's busy for 15 cycles, and the second kernel took twice as long with them.)
+struct F2 {
+  float hi, lo;
+};
+__device__ __forceinline__ F2 sum_of(float a, float b) {
+  const float s = __fadd_rn(a, b), t = __fsub_rn(s, a);
+  return {s, __fadd_rn(__fsub_rn(a, __fsub_rn(s, t)), __fsub_rn(b, t))};
+}
+__device__ __forceinline__ F2 plus(F2 a, float b) {
+  const F2 s = sum_of(a.hi, b);
+  const float e = __fadd_rn(s.lo, a.lo), hi = __fadd_rn(s.hi, e);
+  return {hi, __fsub_rn(e, __fsub_rn(hi, s.hi))};
+}
+
+// Quarters of scores (which stay in fp32's range) as integers of the same order; 0 for what is no candidate.
 using Key = unsigned long long;
-__device__ __forceinline__ Key key_of(double s) {
-  const long long b = __double_as_longlong(s);
-  if (!(s > -CUDART_INF)) return 0;
-  return b < 0 ? ~static_cast<Key>(b) : static_cast<Key>(b) | 0x8000000000000000ull;
+__device__ __forceinline__ Key key_of(float x, F2 off) {
+  if (!(x > -CUDART_INF_F) || off.hi == -CUDART_INF_F) return 0;
+  const F2 s = plus(off, 0.25f * x);
+  return static_cast<Key>(float_order_key(s.hi)) << 32 | float_order_key(s.lo);
 }
-__device__ __forceinline__ double score_of(Key k) {
-  return __longlong_as_double(static_cast<long long>(k >> 63 ? k & 0x7FFFFFFFFFFFFFFFull : ~k));
+__device__ __forceinline__ float score_of(Key k) {
+  const uint32_t u = static_cast<uint32_t>(k >> 32);
+  return 4.f * __uint_as_float(u >> 31 ? u & 0x7FFFFFFFu : ~u);
 }
+// A quarter of m + log s, s at least 1, to 2^-24: the log of s is that of a power of two and of a number in [1, 2).
+__device__ __forceinline__ F2 quarter_lse(float m, float s) {
+  constexpr float kHi = 0x1.62e4p-1f, kLo = 1.42860682e-6f;   // ln 2, the first with 15 bits
+  const int bits = __float_as_int(s), e = (bits >> 23) - 127;
+  const float f = __int_as_float((bits & 0x007FFFFF) | 0x3F800000);
+  return plus(plus(sum_of(0.25f * m, e * (0.25f * kHi)), e * (0.25f * kLo)), 0.25f * logf(f));
+}
+
+// What a search may leave: groups, lines, elements.  `key` has room for the lines of as many groups at least.
+constexpr int kListed = 256, kElements = 1024, kMinRoom = kListed * kLines;
 
 struct SmemBeam {
-  Key key[kKept];
-  double off[kMaxBeams];     // cum - lse; -infinity for a beam without candidates
-  int list[kMaxBest], sorted[kMaxBest], from[kMaxBest];
-  Key best[kMaxBest];
+  F2 off[kMaxBeams];         // a quarter of cum - lse; -infinity for a beam without candidates
+  int groups[kListed], lines[kListed];
+  Key best[kElements];       // the elements that are left
+  int place[kElements];
+  int list[kMaxBest], sorted[kMaxBest];
   Key lo[kWarps], hi[kWarps];
   int count[2][kWarps];
+  int left[3];               // groups, lines, elements that reach the score
   int n;
-  int last;
+  uint32_t key[kMinRoom];    // high halves of the keys of the items that are searched (more, for many groups)
 };
 
 // The sum of every thread's x; `turn` alternates between calls in a row.
@@ -132,30 +193,47 @@ __device__ __forceinline__ int block_sum(SmemBeam& S, int x, int& turn) {
   turn ^= 1;
   if ((threadIdx.x & 31) == 0) S.count[turn][threadIdx.x >> 5] = x;
   __syncthreads();
-  int s = 0;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) s += S.count[turn][w];
-  return s;
+  return __reduce_add_sync(0xffffffffu, (threadIdx.x & 31) < kWarps ? S.count[turn][threadIdx.x & 31] : 0);
+}
+
+// A half key that at least K of the n in S.key reach (0 is none), 1 if there are fewer, and at most `most` where they differ
+// enough.  Each thread comes with the least, largest and number of keys of its own.  A search by halves.
+__device__ __noinline__ uint32_t threshold(SmemBeam& S, int n, int K, int most, int& turn, uint32_t lo, uint32_t hi, int mine) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  lo = __reduce_min_sync(0xffffffffu, lo);
+  hi = __reduce_max_sync(0xffffffffu, hi);
+  if (lane == 0) S.lo[warp] = lo, S.hi[warp] = hi;
+  int c = block_sum(S, mine, turn);     // keys that reach lo
+  lo = __reduce_min_sync(0xffffffffu, lane < kWarps ? static_cast<uint32_t>(S.lo[lane]) : lo);
+  hi = __reduce_max_sync(0xffffffffu, lane < kWarps ? static_cast<uint32_t>(S.hi[lane]) : hi);
+  if (c < K) return 1;
+  while (c > most && lo < hi) {
+    const uint32_t mid = lo + (hi - lo + 1) / 2;
+    int x = 0;
+    for (int i = tid; i < n; i += kThreads) x += S.key[i] >= mid;
+    x = block_sum(S, x, turn);
+    if (x >= K) lo = mid, c = x;
+    else hi = mid - 1;
+  }
+  return lo;
 }
 
 // The first min(K, candidates) of n items by key, then index: their indices, ascending, to S.sorted.  Returns how many.
-// A search by halves over keys; where keys are equal at the end, one over indices.
+// Searches by halves over keys, which are formed anew at each look, then for equal ones over indices.
 template <typename F>
 __device__ int select_best(SmemBeam& S, int n, int K, F make) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const bool kept = n <= kKept;
+  int turn = 0;
+  auto count = [&](auto which) {
+    int x = 0;
+    for (int i = tid; i < n; i += kThreads) x += which(make(i), i);
+    return block_sum(S, x, turn);
+  };
   Key lo = ~0ull, hi = 0;
-  int mine = 0, turn = 0;
   for (int i = tid; i < n; i += kThreads) {
     const Key k = make(i);
-    if (kept) S.key[i] = k;
-    if (k) {
-      ++mine;
-      lo = min(lo, k);
-      hi = max(hi, k);
-    }
+    if (k) lo = min(lo, k), hi = max(hi, k);
   }
-  auto get = [&](int i) { return kept ? S.key[i] : make(i); };
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) {
     lo = min(lo, __shfl_xor_sync(0xffffffffu, lo, o));
@@ -163,41 +241,28 @@ __device__ int select_best(SmemBeam& S, int n, int K, F make) {
   }
   if (lane == 0) S.lo[warp] = lo, S.hi[warp] = hi;
   if (tid == 0) S.n = 0;
-  const int some = block_sum(S, mine, turn);
-#pragma unroll
+  int c = count([](Key k, int) { return k != 0; });
   for (int w = 0; w < kWarps; ++w) lo = min(lo, S.lo[w]), hi = max(hi, S.hi[w]);
-  const int want = min(K, some);
-  if (want == 0) {
-    __syncthreads();
-    return 0;
-  }
-  int until = n;    // of the items with the key lo, those with indices below this one
-  int c = some;     // items with keys from lo on
+  const int want = min(K, c);
+  if (want == 0) return 0;
   while (c > want && lo < hi) {
     const Key mid = lo + (hi - lo + 1) / 2;
-    int x = 0;
-    for (int i = tid; i < n; i += kThreads) x += get(i) >= mid;
-    x = block_sum(S, x, turn);
+    const int x = count([&](Key k, int) { return k >= mid; });
     if (x >= want) lo = mid, c = x;
     else hi = mid - 1;
   }
-  if (c > want) {   // more items with the key lo than there is room for
+  int until = n;    // of the items with the key lo, those with indices below this one
+  if (c > want) {
     int a = 0, b = n;    // the smallest `until` that leaves enough lies in (a, b]
     while (b - a > 1) {
       const int mid = (a + b) / 2;
-      int x = 0;
-      for (int i = tid; i < n; i += kThreads) {
-        const Key k = get(i);
-        x += k > lo || (k == lo && i < mid);
-      }
-      x = block_sum(S, x, turn);
-      if (x >= want) b = mid;
+      if (count([&](Key k, int i) { return k > lo || (k == lo && i < mid); }) >= want) b = mid;
       else a = mid;
     }
     until = b;
   }
   for (int i = tid; i < n; i += kThreads) {
-    const Key k = get(i);
+    const Key k = make(i);
     if (k > lo || (k == lo && i < until)) S.list[atomicAdd(&S.n, 1)] = i;
   }
   __syncthreads();
@@ -211,210 +276,327 @@ __device__ int select_best(SmemBeam& S, int n, int K, F make) {
   return want;
 }
 
-// A request's K best from its groups' maxima and sums.
+// Where item i of a request's groups, of the lines of listed groups and of the elements of listed lines lies, and its key.
 template <typename T>
-__device__ void finish(SmemBeam& S, const BeamParams& p, int b) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int64_t g0 = int64_t(b) * p.W * p.groups;   // the request's first group
-  for (int w = warp; w < p.W; w += kWarps) {
-    const float2* g = p.group + g0 + int64_t(w) * p.groups;
-    const float cum = p.cum[b * p.W + w];
-    float m = -CUDART_INF_F;
-    for (int i = lane; i < p.groups; i += 32) m = fmaxf(m, __ldcg(&g[i].x));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    double s = 0;
-    for (int i = lane; i < p.groups; i += 32) {
-      const float2 x = __ldcg(&g[i]);
-      if (x.y != 0.f) s += static_cast<double>(x.y) * expf(x.x - m);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    if (lane == 0) {
-      const bool bad = !(cum < CUDART_INF_F) || !(s < CUDART_INF);   // NaN or +infinity among the logits or as score
-      flag_error(p.err, bad ? SPKV_DEVERR_BEAM : 0u);
-      S.off[w] = bad || s == 0 || cum == -CUDART_INF_F ? -CUDART_INF : static_cast<double>(cum) - (m + log(s));
-    }
+struct Items {
+  const BeamParams& p;
+  const F2* off;
+  int b;
+  static constexpr int kEach = kLineBytes / sizeof(T);
+  __device__ __forceinline__ int64_t first() const { return int64_t(b) * p.W * p.groups; }   // the request's first group
+  __device__ __forceinline__ Key group(int g) const {
+    return key_of(p.group[first() + g].x, off[g / p.groups]);
   }
-  __syncthreads();
-  // groups of all beams
-  const int ng = select_best(S, p.W * p.groups, p.K, [&](int i) {
-    const double off = S.off[i / p.groups];
-    return off == -CUDART_INF ? Key(0) : key_of(__ldcg(&p.group[g0 + i].x) + off);
-  });
-  if (tid < ng) S.from[tid] = S.sorted[tid];
-  __syncthreads();
-  // their lines
-  const int nl = select_best(S, ng * kLines, p.K, [&](int i) {
-    const int g = S.from[i / kLines];
-    return key_of(__ldcg(&p.line_max[(g0 + g) * kLines + i % kLines]) + S.off[g / p.groups]);
-  });
-  int line = 0;   // thread t's: group * kLines + line of the t-th line
-  if (tid < nl) line = S.from[S.sorted[tid] / kLines] * kLines + S.sorted[tid] % kLines;
-  __syncthreads();
-  if (tid < nl) S.from[tid] = line;
-  __syncthreads();
-  // their elements
-  constexpr int kEach = kLineBytes / sizeof(T);
-  auto look = [&](int i, int& w, int& token) {
-    const int x = S.from[i / kEach], g = x / kLines;
-    w = g / p.groups;
-    token = ((g - w * p.groups) * kLines + x % kLines) * kEach + i % kEach;
-    if (token >= p.V) return Key(0);
-    return key_of(Traits<T>::one(reinterpret_cast<const T*>(p.logits + (int64_t(b) * p.W + w) * p.row_bytes) + token) + S.off[w]);
-  };
-  const int n = select_best(S, nl * kEach, p.K, [&](int i) {
-    int w, token;
-    return look(i, w, token);
-  });
-  int w = -1, token = -1;
-  Key k = 0;
-  if (tid < n) {
-    k = look(S.sorted[tid], w, token);
-    S.best[tid] = k;
+  // line: group * kLines + its line of the group
+  __device__ __forceinline__ Key line(int x) const {
+    return key_of(p.line_max[first() * kLines + x], off[x / kLines / p.groups]);
   }
-  __syncthreads();
-  if (tid < p.K) {
-    int at = tid;
-    if (tid < n) {
-      at = 0;
-      for (int j = 0; j < n; ++j) at += S.best[j] > k || (S.best[j] == k && j < tid);
-    }
-    const int64_t o = int64_t(b) * p.K + at;
-    p.tokens[o] = token;
-    p.parents[o] = w;
-    p.scores[o] = tid < n ? static_cast<float>(score_of(k)) : -CUDART_INF_F;
+  // element e of line x; place: beam * V + token
+  __device__ __forceinline__ Key element(int x, int e, int& place) const {
+    const int w = x / kLines / p.groups, token = (x - w * p.groups * kLines) * kEach + e;
+    place = w * p.V + token;
+    if (token >= p.V) return 0;
+    return key_of(Traits<T>::one(reinterpret_cast<const T*>(p.logits + (int64_t(b) * p.W + w) * p.row_bytes) + token), off[w]);
+  }
+};
+
+// The K best of n elements in S.best, S.place to the outputs, -1, -1, -infinity behind them: a warp counts what is ahead of
+// an element.
+__device__ __forceinline__ void write_best(SmemBeam& S, const BeamParams& p, int b, int n) {
+  const int64_t o = int64_t(b) * p.K;
+  const int lane = threadIdx.x & 31;
+  for (int i = threadIdx.x >> 5; i < n; i += kWarps) {
+    const Key k = S.best[i];
+    const int place = S.place[i];
+    int at = 0;
+    for (int j = lane; j < n; j += 32) at += S.best[j] > k || (S.best[j] == k && S.place[j] < place);
+    at = __reduce_add_sync(0xffffffffu, at);
+    if (lane || at >= p.K) continue;
+    const int w = place / p.V;
+    p.tokens[o + at] = place - w * p.V;
+    p.parents[o + at] = w;
+    p.scores[o + at] = score_of(k);
+  }
+  for (int i = n + threadIdx.x; i < p.K; i += kThreads) {
+    p.tokens[o + i] = p.parents[o + i] = -1;
+    p.scores[o + i] = -CUDART_INF_F;
   }
 }
 
 constexpr int kVec = kGroupBytes / 512;   // 16-byte vectors of a lane
 
-// The 16 bytes at `at` (16-byte aligned), elements outside [begin, end) as -infinity, which are not read.
-template <typename T>
-__device__ __forceinline__ uint4 load_inside(const uint8_t* at, const uint8_t* begin, const uint8_t* end) {
-  if (at >= begin && at + 16 <= end) return *reinterpret_cast<const uint4*>(at);
-  constexpr uint32_t none = Traits<T>::kNegInf;
-  uint32_t word[4] = {none, none, none, none};
-#pragma unroll
-  for (int j = 0; j < 16 / static_cast<int>(sizeof(T)); ++j) {
-    const uint8_t* e = at + j * sizeof(T);
-    if (e < begin || e >= end) continue;
-    if constexpr (sizeof(T) == 4) {
-      word[j] = *reinterpret_cast<const uint32_t*>(e);
-    } else {
-      const uint32_t x = *reinterpret_cast<const uint16_t*>(e);
-      word[j / 2] = j & 1 ? (word[j / 2] & 0xFFFFu) | x << 16 : (word[j / 2] & 0xFFFF0000u) | x;
-    }
-  }
-  return make_uint4(word[0], word[1], word[2], word[3]);
-}
+// A group's bytes in shared memory, from the 16-byte border at or before its first one on.
+constexpr int kStage = kGroupBytes + 16;
 
-// Vectors that begin Q words (and half a word) into the aligned ones v, in place: what lies behind a lane's own vector is
-// the next lane's, for the last lane the first lane's of the next k (`last` for the last k).
-template <int Q, bool HALF>
-__device__ __forceinline__ void shift(uint4 (&v)[kVec], uint4 last, int lane) {
-  constexpr int need = Q + (HALF ? 1 : 0);
-#pragma unroll
-  for (int k = 0; k < kVec; ++k) {
-    const uint4 mine = v[k], next = k + 1 < kVec ? v[k + 1 < kVec ? k + 1 : k] : last;
-    const uint32_t give[4] = {lane ? mine.x : next.x, lane ? mine.y : next.y, lane ? mine.z : next.z, lane ? mine.w : next.w};
-    uint32_t w[9] = {mine.x, mine.y, mine.z, mine.w, 0, 0, 0, 0, 0};
-#pragma unroll
-    for (int j = 0; j < need; ++j) w[4 + j] = __shfl_sync(0xffffffffu, give[j], (lane + 1) & 31);
-    uint32_t o[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) o[j] = HALF ? __byte_perm(w[Q + j], w[Q + j + 1], 0x5432) : w[Q + j];
-    v[k] = make_uint4(o[0], o[1], o[2], o[3]);
-  }
-}
-
-// A group's 4 KiB at `from`, which may begin at any element, of the row [begin, end): vector k of the lane holds the bytes
-// from 512 k + 16 lane on, -infinity behind the row.
+// Asks for the group `from` of the row [begin, end), nothing outside the row.  By a warp.
 template <typename T>
-__device__ __forceinline__ void load_group(uint4 (&v)[kVec], const uint8_t* from, const uint8_t* begin, const uint8_t* end, int lane) {
+__device__ __forceinline__ void ask(uint8_t* stage, const uint8_t* from, const uint8_t* begin, const uint8_t* end, int lane) {
   const int off = static_cast<int>(reinterpret_cast<uintptr_t>(from) & 15);
   const uint8_t* const at = from - off + lane * 16;
-  const uint8_t* const stop = from - off + kGroupBytes;   // the first vector behind the lanes', of which a part is the group's
-  uint4 last = make_uint4(0, 0, 0, 0);
-  if (from - off >= begin && stop + (off ? 16 : 0) <= end) {
+  const uint32_t to = smem_u32(stage) + lane * 16;
+  if (from - off >= begin && from - off + kStage <= end) {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k)
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + k * 512), "l"(at + k * 512) : "memory");
+    if (lane == 0) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + kGroupBytes), "l"(at + kGroupBytes) : "memory");
+    return;
+  }
+  auto copy = [&](int x) {   // 16 bytes from x on, zeros behind the row
+    const int64_t left = end - (at + x);
+    const int n = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + x), "l"(n ? at + x : from - off + 16), "r"(n) : "memory");
+  };
+  const bool head = at < begin;   // the row begins inside its first 16 bytes
+#pragma unroll
+  for (int k = 0; k < kVec; ++k)
+    if (k > 0 || !head) copy(k * 512);
+  if (lane == 0 && off) copy(kGroupBytes);
+  if (head)
+    for (const uint8_t* e = begin; e < at + 16 && e < end; e += sizeof(T)) *reinterpret_cast<T*>(stage + (e - at)) = *reinterpret_cast<const T*>(e);
+}
+
+// A group that has arrived: vector k of the lane holds the bytes from 512 k + 16 lane on, elements from `left` on as -infinity.
+template <typename T>
+__device__ __forceinline__ void take(uint4 (&v)[kVec], const uint8_t* stage, int off, int left, int lane) {
+  const uint8_t* const at = stage + off + lane * 16;
+  if (off == 0) {
 #pragma unroll
     for (int k = 0; k < kVec; ++k) v[k] = *reinterpret_cast<const uint4*>(at + k * 512);
-    if (off && lane == 0) last = *reinterpret_cast<const uint4*>(stop);
   } else {
+    const bool half = sizeof(T) == 2 && (off & 2);
+    const uint32_t* w = reinterpret_cast<const uint32_t*>(at - (half ? 2 : 0));
+    const uint32_t pick = half ? 0x5432 : 0x3210;
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) v[k] = load_inside<T>(at + k * 512, begin, end);
-    if (off && lane == 0) last = load_inside<T>(stop, begin, end);
-  }
-  // (a row that begins at the same place as its neighbours' lines goes one way for all its groups)
-  if (off & 2) {
-    if constexpr (sizeof(T) == 2) {
-      switch (off >> 2) {
-        case 0: return shift<0, true>(v, last, lane);
-        case 1: return shift<1, true>(v, last, lane);
-        case 2: return shift<2, true>(v, last, lane);
-        default: return shift<3, true>(v, last, lane);
-      }
+    for (int k = 0; k < kVec; ++k) {
+      const uint32_t a = w[k * 128], b = w[k * 128 + 1], c = w[k * 128 + 2], d = w[k * 128 + 3];
+      const uint32_t e = half ? w[k * 128 + 4] : 0;
+      v[k] = make_uint4(__byte_perm(a, b, pick), __byte_perm(b, c, pick), __byte_perm(c, d, pick), __byte_perm(d, e, pick));
     }
   }
-  switch (off >> 2) {
-    case 0: return;
-    case 1: return shift<1, false>(v, last, lane);
-    case 2: return shift<2, false>(v, last, lane);
-    default: return shift<3, false>(v, last, lane);
+  constexpr int kPer = 16 / sizeof(T);
+  if (left < kGroupBytes / static_cast<int>(sizeof(T))) {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) {
+      const int n = left - k * (512 / static_cast<int>(sizeof(T))) - lane * kPer;   // elements of the vector that exist
+      uint32_t w[4] = {v[k].x, v[k].y, v[k].z, v[k].w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        if constexpr (sizeof(T) == 4) {
+          if (j >= n) w[j] = Traits<T>::kNegInf;
+        } else {
+          if (2 * j + 1 >= n) w[j] = 2 * j >= n ? Traits<T>::kNegInf : (w[j] & 0xFFFFu) | (Traits<T>::kNegInf & 0xFFFF0000u);
+        }
+      }
+      v[k] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
+// A group's maxima of lines, its own and its sum, from the lane's vectors.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 4) beam_select_kernel(const __grid_constant__ BeamParams p) {
-  __shared__ SmemBeam S;
+__device__ __forceinline__ void look_at_group(const BeamParams& p, const uint4 (&v)[kVec], int64_t i, int lane) {
+  // vector k of eight lanes is line 4 k + lane / 8; each lane ends with that of k = lane % 8
+  float m[kVec];
+#pragma unroll
+  for (int k = 0; k < kVec; ++k) m[k] = Traits<T>::top(v[k]);
+#pragma unroll
+  for (int o = 4; o > 0; o >>= 1) {
+#pragma unroll
+    for (int k = 0; k < o; ++k) {
+      const bool up = lane & o;
+      const float give = up ? m[k] : m[k + o], keep = up ? m[k + o] : m[k];
+      m[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
+    }
+  }
+  p.line_max[i * kLines + 4 * (lane & 7) + (lane >> 3)] = m[0];
+  float top = m[0];
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  float s = 0.f;
+  if (fabsf(top) < 0x1p126f) {
+    const float c = __fmul_rn(top, kLog2e);
+    float s0 = 0.f, s1 = 0.f;
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) add_exps<T>(s0, s1, v[k], c);
+    s = (s0 + s1) * ex2(-fmaf(top, kLog2e, -c));   // what c was rounded by
+  } else {
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) s += far_exps<T>(v[k], top);
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  if (lane == 0) p.group[i] = make_float2(top, s);
+}
+
+// A warp takes groups a grid of warps apart, with kStages - 1 of them on their way.
+template <typename T>
+__global__ void __launch_bounds__(kGroupThreads, kCtasPerSm) beam_groups_kernel(const __grid_constant__ BeamParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint8_t* const mine = smem_raw + warp * kStages * kStage;
+  const int step = gridDim.x * (kGroupThreads / 32), step_row = step / p.groups, step_g = step % p.groups;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / p.ctas, i = (blockIdx.x % p.ctas) * kWarps + warp;   // group of the request
-  if (i < p.W * p.groups) {
-    const int w = i / p.groups, g = i - w * p.groups;
-    const int64_t row = int64_t(b) * p.W + w, at_group = row * p.groups + g;
-    const uint8_t* const r0 = p.logits + row * p.row_bytes;
-    const uint8_t* const end = r0 + int64_t(p.V) * sizeof(T);
-    const uint8_t* const from = r0 + int64_t(g) * kGroupBytes;
-    float top = -CUDART_INF_F, sum = 0.f;
-    if (p.cum[row] != -CUDART_INF_F) {   // a beam that ended is not read
-      uint4 v[kVec];
-      load_group<T>(v, from, r0, end, lane);
-      // maxima of lines: vector k of eight lanes is line 4 k + lane / 8; each lane ends with that of k = lane % 8
-      float m[kVec];
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) m[k] = Traits<T>::top(v[k]);
-#pragma unroll
-      for (int o = 4; o > 0; o >>= 1) {
-#pragma unroll
-        for (int k = 0; k < o; ++k) {
-          const bool up = lane & o;
-          const float give = up ? m[k] : m[k + o], keep = up ? m[k + o] : m[k];
-          m[k] = fmaxf(keep, __shfl_xor_sync(0xffffffffu, give, o));
-        }
-      }
-      p.line_max[at_group * kLines + 4 * (lane & 7) + (lane >> 3)] = m[0];
-      top = m[0];
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-      const float ref = top == -CUDART_INF_F ? 0.f : top;
-#pragma unroll
-      for (int k = 0; k < kVec; ++k) sum += exps_of<T>(v[k], ref);
-#pragma unroll
-      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  struct Place {
+    int row, g;
+  };
+  // moves to the first group from x on of a beam that has not ended (one that has is not read, nor what would be written of it)
+  auto forward = [&](Place x) {
+    x.row += step_row;
+    x.g += step_g;
+    if (x.g >= p.groups) x.g -= p.groups, ++x.row;
+    return x;
+  };
+  auto live = [&](Place x) {
+    while (x.row < p.rows && p.cum[x.row] == -CUDART_INF_F) x = forward(x);
+    return x;
+  };
+  const int first = blockIdx.x * (kGroupThreads / 32) + warp;
+  Place next = live({first / p.groups, first % p.groups});   // to be asked for
+  Place queue[kStages - 1];
+  auto ask_next = [&](int s) {
+    const Place x = next;
+    if (x.row < p.rows) {
+      const uint8_t* const r0 = p.logits + x.row * p.row_bytes;
+      ask<T>(mine + s * kStage, r0 + int64_t(x.g) * kGroupBytes, r0, r0 + int64_t(p.V) * sizeof(T), lane);
+      next = live(forward(x));
     }
-    if (lane == 0) p.group[at_group] = make_float2(top, sum);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    return x;
+  };
+#pragma unroll
+  for (int s = 0; s < kStages - 1; ++s) queue[s] = ask_next(s);
+  for (int s = 0; queue[0].row < p.rows; s = s + 1 == kStages ? 0 : s + 1) {
+    const Place x = queue[0];
+    asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+    __syncwarp();   // every lane's copies are there, and every lane is through with the stage before
+#pragma unroll
+    for (int k = 0; k + 1 < kStages - 1; ++k) queue[k] = queue[k + 1];
+    queue[kStages - 2] = ask_next(s == 0 ? kStages - 1 : s - 1);
+    uint4 v[kVec];
+    const uint8_t* const r0 = p.logits + x.row * p.row_bytes;
+    take<T>(v, mine + s * kStage, static_cast<int>(reinterpret_cast<uintptr_t>(r0) & 15),   // (a group is a multiple of 16 bytes)
+            p.V - x.g * (kGroupBytes / static_cast<int>(sizeof(T))), lane);
+    look_at_group<T>(p, v, int64_t(x.row) * p.groups + x.g, lane);
+  }
+}
+
+// A CTA a request: its K best from its groups' maxima and sums.
+template <typename T>
+__global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_constant__ BeamParams p) {
+  extern __shared__ __align__(16) uint8_t smem_raw[];
+  SmemBeam& S = *reinterpret_cast<SmemBeam*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.x;
+  if (tid < 3) S.left[tid] = 0;
+  pdl_wait();
+  pdl_trigger();
+  const Items<T> it{p, S.off, b};
+  // ---- a warp a beam: its log of the sum of exponentials, its groups' keys
+  uint32_t lo = ~0u, hi = 0;
+  int mine = 0;
+  auto keep = [&](int i, Key k) {
+    const uint32_t half = static_cast<uint32_t>(k >> 32);
+    S.key[i] = half;
+    if (half) ++mine, lo = min(lo, half), hi = max(hi, half);
+  };
+  for (int w = warp; w < p.W; w += kWarps) {
+    const float2* g = p.group + it.first() + int64_t(w) * p.groups;
+    const float cum = p.cum[b * p.W + w];
+    // the first groups of a lane are asked for at once, and with the score
+    constexpr int kFew = 4;
+    float2 x[kFew];
+#pragma unroll
+    for (int k = 0; k < kFew; ++k) x[k] = lane + 32 * k < p.groups ? g[lane + 32 * k] : make_float2(-CUDART_INF_F, 0.f);
+    F2 off{-CUDART_INF_F, 0.f};
+    if (cum != -CUDART_INF_F) {
+      float m = fmaxf(fmaxf(x[0].x, x[1].x), fmaxf(x[2].x, x[3].x));
+      for (int i = lane + 32 * kFew; i < p.groups; i += 32) m = fmaxf(m, g[i].x);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+      float s = 0.f;
+      auto add = [&](float2 y) { s += y.y == 0.f ? 0.f : y.y * expf(y.x - m); };   // (-infinity - m may be no number)
+#pragma unroll
+      for (int k = 0; k < kFew; ++k) add(x[k]);
+      for (int i = lane + 32 * kFew; i < p.groups; i += 32) add(g[i]);
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      const bool bad = !(cum < CUDART_INF_F) || !(s < CUDART_INF_F);   // NaN or +infinity among the logits or as score
+      if (bad && lane == 0) flag_error(p.err, SPKV_DEVERR_BEAM);
+      if (!bad && s > 0.f) {
+        const F2 lse = quarter_lse(m, s);
+        off = plus(sum_of(0.25f * cum, -lse.hi), -lse.lo);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kFew; ++k)
+      if (lane + 32 * k < p.groups) keep(w * p.groups + lane + 32 * k, key_of(x[k].x, off));
+    for (int i = lane + 32 * kFew; i < p.groups; i += 32) keep(w * p.groups + i, key_of(g[i].x, off));
+    if (lane == 0) S.off[w] = off;
+  }
+  const int n = p.W * p.groups, most = p.K + max(p.K / 2, 8);
+  int turn = 0;
+  // ---- the groups that reach a score that K groups reach (all, if there are fewer)
+  uint32_t t = threshold(S, n, p.K, most, turn, lo, hi, mine);
+  for (int i = tid; i < n; i += kThreads) {
+    if (S.key[i] < t) continue;
+    const int x = atomicAdd(&S.left[0], 1);
+    if (x < kListed) S.groups[x] = i;
   }
   __syncthreads();
-  if (tid == 0) {
-    int before;   // release: this CTA's groups, which the barrier has ordered before; acquire: the others'
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + b) : "memory");
-    S.last = before == p.ctas - 1;
-    if (S.last) p.arrived[b] = 0;
+  auto line_of = [&](int i) { return S.groups[i / kLines] * kLines + i % kLines; };
+  bool fits = S.left[0] <= kListed;
+  if (fits) {
+    // ---- their lines that reach it; where those are many (groups that are much alike, or few), that reach a score that
+    // K lines reach
+    const int lines = S.left[0] * kLines;
+    lo = ~0u, hi = 0, mine = 0;
+    auto collect = [&](int i) {
+      if (S.key[i] < t) return;
+      const int at = atomicAdd(&S.left[1], 1);
+      if (at < kListed) S.lines[at] = line_of(i);
+    };
+    for (int i = tid; i < lines; i += kThreads) {
+      keep(i, it.line(line_of(i)));
+      collect(i);
+    }
+    __syncthreads();
+    if (S.left[1] > 2 * most) {
+      t = threshold(S, lines, p.K, most, turn, lo, hi, mine);
+      if (tid == 0) S.left[1] = 0;
+      __syncthreads();
+      for (int i = tid; i < lines; i += kThreads) collect(i);
+      __syncthreads();
+    }
+    fits = S.left[1] <= kListed;
+  }
+  if (fits) {
+    // ---- their elements that reach it
+    for (int i = tid; i < S.left[1] * it.kEach; i += kThreads) {
+      int place;
+      const Key k = it.element(S.lines[i / it.kEach], i % it.kEach, place);
+      if (k >> 32 < t) continue;
+      const int at = atomicAdd(&S.left[2], 1);
+      if (at < kElements) S.best[at] = k, S.place[at] = place;
+    }
+    __syncthreads();
+    if (S.left[2] <= kElements) return write_best(S, p, b, S.left[2]);
+  }
+  // ---- too many alike: exactly K groups, of their lines exactly K, of those lines' elements
+  __syncthreads();
+  const int ng = select_best(S, n, p.K, [&](int i) { return it.group(i); });
+  if (tid < ng) S.groups[tid] = S.sorted[tid];
+  __syncthreads();
+  const int nl = select_best(S, ng * kLines, p.K, [&](int i) { return it.line(line_of(i)); });
+  if (tid < nl) S.lines[tid] = line_of(S.sorted[tid]);
+  __syncthreads();
+  int place;
+  const int ne = select_best(S, nl * it.kEach, p.K, [&](int i) { return it.element(S.lines[i / it.kEach], i % it.kEach, place); });
+  if (tid < ne) {
+    S.best[tid] = it.element(S.lines[S.sorted[tid] / it.kEach], S.sorted[tid] % it.kEach, place);
+    S.place[tid] = place;
   }
   __syncthreads();
-  if (S.last) finish<T>(S, p, b);
+  write_best(S, p, b, ne);
 }
 
 // ---------------------------------------------------------------------------------------------- reordering
@@ -558,6 +740,7 @@ __global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant
 }  // namespace
 }  // namespace spkv
 
+using spkv::kCtasPerSm;
 using spkv::kGroupBytes;
 using spkv::kMaxBeams;
 using spkv::kMaxBest;
@@ -569,16 +752,32 @@ bool on_device(int device) {
   return cudaGetDevice(&dev) == cudaSuccess && dev == device;
 }
 
+size_t smem_of(int64_t keys) {
+  return sizeof(spkv::SmemBeam) + sizeof(uint32_t) * (std::max(keys, int64_t(spkv::kMinRoom)) - spkv::kMinRoom);
+}
+
 template <typename T>
-cudaError_t launch_select_beams(const spkv::BeamParams& p, int B, cudaStream_t st) {
-  return spkv::launch_pdl(spkv::beam_select_kernel<T>, dim3(static_cast<unsigned>(B) * p.ctas), dim3(spkv::kThreads), 0, st, p);
+cudaError_t launch_select_beams(const spkv::BeamParams& p, int B, int sms, cudaStream_t st) {
+  constexpr int each = spkv::kGroupThreads / 32;
+  const int ctas = std::min((p.rows * p.groups + each - 1) / each, kCtasPerSm * sms);
+  const cudaError_t e = spkv::launch_pdl(spkv::beam_groups_kernel<T>, dim3(ctas), dim3(spkv::kGroupThreads), each * spkv::kStages * spkv::kStage, st, p);
+  if (e != cudaSuccess) return e;
+  return spkv::launch_pdl(spkv::beam_best_kernel<T>, dim3(B), dim3(spkv::kThreads), smem_of(int64_t(p.W) * p.groups), st, p);
+}
+
+template <typename T>
+cudaError_t allow_smem() {
+  const cudaError_t e = cudaFuncSetAttribute(spkv::beam_groups_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                             spkv::kGroupThreads / 32 * spkv::kStages * spkv::kStage);
+  if (e != cudaSuccess) return e;
+  return cudaFuncSetAttribute(spkv::beam_best_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem_of(spkv::kMaxGroups)));
 }
 
 }  // namespace
 
 extern "C" {
 
-int beam_plan_create(spkv_cache_t c, int max_rows, int max_vocab, void* stream, spkv_beam_plan_t* out) {
+int beam_plan_create(spkv_cache_t c, int max_rows, int max_vocab, spkv_beam_plan_t* out) {
   if (!out) return SPKV_EINVAL;
   *out = nullptr;
   if (!c || max_rows <= 0 || max_vocab <= 0 || !on_device(c->device)) return SPKV_EINVAL;
@@ -590,10 +789,11 @@ int beam_plan_create(spkv_cache_t c, int max_rows, int max_vocab, void* stream, 
   p->max_vocab = max_vocab;
   p->max_groups = static_cast<int>((int64_t(max_vocab) * 4 + kGroupBytes - 1) / kGroupBytes);   // of fp32 rows
   const int64_t n = int64_t(max_rows) * p->max_groups;
-  const bool ok = cudaMalloc(&p->line_max, n * 32 * sizeof(float)) == cudaSuccess && cudaMalloc(&p->group, n * sizeof(float2)) == cudaSuccess &&
-                  cudaMalloc(&p->arrived, max_rows * sizeof(int32_t)) == cudaSuccess &&
-                  cudaMemsetAsync(p->arrived, 0, max_rows * sizeof(int32_t), static_cast<cudaStream_t>(stream)) == cudaSuccess;
-  if (!ok) {
+  if (allow_smem<float>() != cudaSuccess || allow_smem<__nv_bfloat16>() != cudaSuccess || allow_smem<__half>() != cudaSuccess) {
+    delete p;
+    return SPKV_ECUDA;
+  }
+  if (cudaMalloc(&p->line_max, n * 32 * sizeof(float)) != cudaSuccess || cudaMalloc(&p->group, n * sizeof(float2)) != cudaSuccess) {
     cudaGetLastError();
     beam_plan_destroy(p);
     return SPKV_ENOMEM;
@@ -606,7 +806,6 @@ int beam_plan_destroy(spkv_beam_plan_t p) {
   if (!p) return SPKV_EINVAL;
   cudaFree(p->line_max);
   cudaFree(p->group);
-  cudaFree(p->arrived);
   delete p;
   return SPKV_OK;
 }
@@ -629,20 +828,19 @@ int beam_select(spkv_cache_t c, spkv_beam_plan_t plan, const void* logits, int t
   p.V = V;
   p.K = K;
   p.groups = static_cast<int>((int64_t(V) * es + kGroupBytes - 1) / kGroupBytes);
-  p.ctas = (W * p.groups + spkv::kWarps - 1) / spkv::kWarps;
+  p.rows = B * W;
+  if (int64_t(W) * p.groups > spkv::kMaxGroups || int64_t(B) * W * p.groups > (int64_t(1) << 30)) return SPKV_EUNSUPPORTED;
   p.cum = cum;
   p.tokens = tokens;
   p.parents = parents;
   p.scores = scores;
   p.line_max = plan->line_max;
   p.group = plan->group;
-  p.arrived = plan->arrived;
   p.err = c->dev_err;
-  if (int64_t(B) * p.ctas >= (int64_t(1) << 31)) return SPKV_EUNSUPPORTED;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = type == SPKV_F32    ? launch_select_beams<float>(p, B, st)
-                        : type == SPKV_BF16 ? launch_select_beams<__nv_bfloat16>(p, B, st)
-                                            : launch_select_beams<__half>(p, B, st);
+  const cudaError_t e = type == SPKV_F32    ? launch_select_beams<float>(p, B, c->sm_count, st)
+                        : type == SPKV_BF16 ? launch_select_beams<__nv_bfloat16>(p, B, c->sm_count, st)
+                                            : launch_select_beams<__half>(p, B, c->sm_count, st);
   return e == cudaSuccess ? SPKV_OK : SPKV_ECUDA;
 }
 

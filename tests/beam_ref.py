@@ -15,7 +15,7 @@ def scores64(x, cum):
         if np.isneginf(m):
             continue
         with np.errstate(over="ignore", under="ignore"):
-            out[w] = x[w] + (np.float64(cum[w]) - (m + np.log(np.exp(x[w] - m).sum())))
+            out[w] = ((x[w] - m) - np.log(np.exp(x[w] - m).sum())) + np.float64(cum[w])   # (m may be the lowest number)
     return out
 
 

@@ -24,7 +24,7 @@ P = 4096
 h = f.handle(False, 2, max_units=64)
 plan = ctypes.c_void_p()
 def create(cache=h, rows=8, vocab=1000, out=ctypes.byref(plan)):
-    return f.lib.beam_plan_create(cache, rows, vocab, None, out)
+    return f.lib.beam_plan_create(cache, rows, vocab, out)
 plans = [create(cache=None), create(rows=0), create(vocab=0), create(rows=65537), create(vocab=(1 << 24) + 1), create(out=None), create()]
 f.events()
 def select(cache=h, plan=plan, logits=P, kind=0, stride=1000, B=2, W=4, V=1000, cum=P, K=8, tokens=P, parents=P, scores=P):
@@ -50,7 +50,7 @@ print(json.dumps([plans, selects, none, runs, reorders, none2, run2, f.lib.beam_
     assert all(v == (-6 if k in six else -1) for k, v in {**selects, **reorders}.items()), (selects, reorders)
     assert none == [[], 0, []] and none2 == [[], 0, []]
     for r in runs:
-        assert r[0] == 0 and len(r[1]) == 1 and "beam_select_kernel" in r[1][0]
+        assert r[0] == 0 and len(r[1]) == 2 and "beam_groups_kernel" in r[1][0] and "beam_best_kernel" in r[1][1]
     assert run2[0] == 0 and len(run2[1]) == 1 and "beam_reorder_kernel" in run2[1][0]
 
 
