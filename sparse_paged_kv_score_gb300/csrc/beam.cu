@@ -606,9 +606,9 @@ struct ReorderParams {
   int32_t* table;
   const int32_t* seq_len;
   int W, Hk, np_max;
-  uint8_t* pool[2];              // pages of 64 bytes_row bytes, or of page_bytes that are copied whole
-  int64_t page_bytes;
-  int row_bytes;                 // 0: whole pages
+  uint8_t* pool[2];              // of `planes` pools: page-heads of page_bytes
+  int planes, page_bytes;
+  int row_bytes;                 // of a token in them; 0: page-heads are copied whole
   uint8_t* ksum;
   int ksum_bytes;                // of a page-head
   int32_t* page_cnt;
@@ -617,124 +617,128 @@ struct ReorderParams {
   uint32_t* err;
 };
 
-constexpr int kStrip = 64;   // columns of a table that a CTA permutes
+constexpr int kStrip = 64;      // columns of a table that are permuted together
+constexpr int kCopyThreads = 256, kCopyCtas = 4;
+constexpr int kPieces = 5;      // 16-byte pieces of a page-head that a thread copies at most, of a plane
+static_assert(kPieces * kCopyThreads * 16 >= 16416, "a page-head of any format");
 
-// What a request's beams do: where beam w's part-filled page comes from and whether it has to be copied there.
-struct Family {
+struct SmemReorder {
   int parent[kMaxBeams];
+  int first[kMaxBeams];     // a beam's first child, -1 if that is the beam itself, kMaxBeams if it has none
+  int page[kMaxBeams];      // part-filled pages as they were, and their rows
+  int rows[kMaxBeams];
   int page_of[kMaxBeams];   // the beam whose part-filled page becomes beam w's
+  int copied[kMaxBeams];    // beams whose part-filled page is a copy
+  unsigned keeps[2], used[2], copies[2];   // bits: children that keep a page, beams with children, children with copies
+  int tile[kMaxBeams][kStrip];
 };
 
-// Fills F from the parents of request b; false (and flags) where they cannot be followed.  Called by a whole CTA.
-__device__ bool family(Family& F, const ReorderParams& p, int b, int& full, bool& part, bool report) {
-  const int tid = threadIdx.x, lane = tid & 31;
-  const int L = p.seq_len[int64_t(b) * p.W];
-  full = L / kPageTokens;
-  part = L % kPageTokens != 0;
-  bool ok = L >= 0;
-  uint32_t bad = !ok || full + (part ? 1 : 0) > p.np_max ? SPKV_DEVERR_PAGE_ID : 0u;
-  if (tid < p.W) {
-    const int x = p.parents[int64_t(b) * p.W + tid];
-    F.parent[tid] = x;
-    if (x < -1 || x >= p.W || p.seq_len[int64_t(b) * p.W + tid] != L) bad |= SPKV_DEVERR_BEAM;
-  }
-  if (__syncthreads_or(bad != 0)) {
-    if (report) flag_error(p.err, bad);
-    return false;
-  }
-  if (tid < 32) {
-    // beams with children, children that keep their parent's page: beams lane and lane + 32
-    unsigned long long used = 0, keeps = 0;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int w = lane + 32 * e, x = w < p.W ? F.parent[w] : -1;
-      bool keep = x >= 0 && (x == w || F.parent[x] != x);
-      if (x >= 0 && x != w)
-        for (int j = 0; j < w; ++j) keep = keep && F.parent[j] != x;
-      const unsigned long long bit = x >= 0 ? 1ull << x : 0ull;
-      used |= static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bit))) |
-              static_cast<unsigned long long>(__reduce_or_sync(0xffffffffu, static_cast<unsigned>(bit >> 32))) << 32;
-      keeps |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, keep)) << (32 * e);
-    }
-    const unsigned long long all = p.W == 64 ? ~0ull : (1ull << p.W) - 1, free = all & ~used;
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int w = lane + 32 * e;
-      if (w >= p.W) continue;
-      int from = F.parent[w];
-      if (!(keeps >> w & 1)) {   // the r-th beam without children
-        int r = __popcll(~keeps & ((1ull << w) - 1));
-        unsigned long long f = free;
-        while (r--) f &= f - 1;
-        from = __ffsll(static_cast<long long>(f)) - 1;
-      }
-      F.page_of[w] = from;
-    }
-  }
-  __syncthreads();
-  return true;
-}
-
-// CTAs 0 .. W Hk - 1 of a request copy beam w's part-filled page of head h; the others permute kStrip columns each.
-__global__ void __launch_bounds__(256) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
-  __shared__ Family F;
-  __shared__ int tile[kMaxBeams][kStrip];
-  __shared__ int last;
+// gridDim.x CTAs a request share its copies (a beam's part-filled page, one head) and its tables' strips; each finds out for
+// itself what the request's beams do.  The last of them to have read the column of part-filled pages writes it.
+__global__ void __launch_bounds__(kCopyThreads, kCopyCtas) beam_reorder_kernel(const __grid_constant__ ReorderParams p) {
+  __shared__ SmemReorder S;
   pdl_wait();
   pdl_trigger();
-  const int tid = threadIdx.x, b = blockIdx.y, x = blockIdx.x, copies = p.W * p.Hk;
-  int full;
-  bool part;
-  const bool ok = family(F, p, b, full, part, x == 0);
-  int32_t* const table = p.table + int64_t(b) * p.W * p.np_max;
-  if (x >= copies) {   // complete pages
-    const int c0 = (x - copies) * kStrip, n = min(kStrip, full - c0);
-    if (!ok || n <= 0) return;
-    for (int i = tid; i < p.W * kStrip; i += blockDim.x)
-      if (i % kStrip < n) tile[i / kStrip][i % kStrip] = table[int64_t(i / kStrip) * p.np_max + c0 + i % kStrip];
-    __syncthreads();
-    for (int i = tid; i < p.W * kStrip; i += blockDim.x) {
-      const int w = i / kStrip, from = F.parent[w];
-      if (i % kStrip < n && from >= 0 && from != w) table[int64_t(w) * p.np_max + c0 + i % kStrip] = tile[from][i % kStrip];
-    }
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y, x = blockIdx.x, W = p.W;
+  int32_t* const table = p.table + int64_t(b) * W * p.np_max;
+  const int L = p.seq_len[int64_t(b) * W], full = L / kPageTokens;
+  const bool part = L % kPageTokens != 0;
+  // ---- who goes on from whom
+  int parent = -1;
+  uint32_t bad = L < 0 || full + (part ? 1 : 0) > p.np_max ? SPKV_DEVERR_PAGE_ID : 0u;
+  if (tid < W) {
+    parent = p.parents[int64_t(b) * W + tid];
+    if (parent < -1 || parent >= W || p.seq_len[int64_t(b) * W + tid] != L) bad |= SPKV_DEVERR_BEAM;
+    S.parent[tid] = parent;
+    S.first[tid] = kMaxBeams;
+  }
+  if (__syncthreads_or(bad != 0)) {
+    if (x == 0) flag_error(p.err, bad);
     return;
   }
-  if (!ok || !part) return;
-  const int w = x / p.Hk, h = x % p.Hk, parent = F.parent[w], mine = F.page_of[w];
-  if (parent >= 0 && mine != parent) {
-    const int src = table[int64_t(parent) * p.np_max + full], dst = table[int64_t(mine) * p.np_max + full];
-    if (src < 0 || src >= p.n_phys || dst < 0 || dst >= p.n_phys) {
-      if (h == 0 && tid == 0) flag_error(p.err, SPKV_DEVERR_PHYS);
-    } else {
-      const int cnt = p.page_cnt ? p.page_cnt[src] : kPageTokens;
-      const int64_t bytes = p.row_bytes ? int64_t(max(0, min(kPageTokens, cnt))) * p.row_bytes : p.page_bytes;
-      const int64_t from = (int64_t(h) * p.n_phys + src) * p.page_bytes, to = (int64_t(h) * p.n_phys + dst) * p.page_bytes;
-#pragma unroll
-      for (int k = 0; k < 2; ++k) {
-        if (!p.pool[k]) continue;
-        for (int64_t i = tid * 16; i < bytes; i += 256 * 16)
-          *reinterpret_cast<uint4*>(p.pool[k] + to + i) = *reinterpret_cast<const uint4*>(p.pool[k] + from + i);
-      }
-      if (p.ksum)
-        for (int i = tid * 16; i < p.ksum_bytes; i += 256 * 16)
-          *reinterpret_cast<uint4*>(p.ksum + (int64_t(h) * p.n_phys + dst) * p.ksum_bytes + i) =
-              *reinterpret_cast<const uint4*>(p.ksum + (int64_t(h) * p.n_phys + src) * p.ksum_bytes + i);
-      if (p.page_cnt && h == 0 && tid == 0) p.page_cnt[dst] = cnt;
+  if (part && tid < W) {   // (the pages' rows are not waited for before the copies need them)
+    S.page[tid] = table[int64_t(tid) * p.np_max + full];
+    if (parent >= 0) atomicMin(&S.first[parent], parent == tid ? -1 : tid);
+  }
+  __syncthreads();
+  if (!part) {
+  } else if (tid < kMaxBeams) {   // two warps
+    const bool keep = tid < W && parent >= 0 && S.first[parent] == (parent == tid ? -1 : tid);
+    const bool used = tid < W && S.first[tid] < kMaxBeams;
+    const unsigned k = __ballot_sync(0xffffffffu, keep), u = __ballot_sync(0xffffffffu, used || tid >= W);
+    const unsigned c = __ballot_sync(0xffffffffu, parent >= 0 && !keep);
+    if (lane == 0) S.keeps[warp] = k, S.used[warp] = u, S.copies[warp] = c;
+    if (tid < W) {
+      const int ph = S.page[tid];
+      S.rows[tid] = !p.page_cnt || ph < 0 || ph >= p.n_phys ? kPageTokens : p.page_cnt[ph];
     }
   }
-  // the last CTA that has read the column of part-filled pages writes it
   __syncthreads();
-  if (tid == 0) {
-    int before;
-    asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + b) : "memory");
-    last = before == copies - 1;
-    if (last) p.arrived[b] = 0;
+  int before = -1;
+  if (part) {
+    // every thread of this CTA has read the column
+    if (tid == kCopyThreads - 1)
+      asm volatile("atom.add.acq_rel.gpu.global.s32 %0, [%1], 1;" : "=r"(before) : "l"(p.arrived + b) : "memory");
+    if (tid < W) {
+      int from = parent;
+      const bool keep = S.keeps[warp] >> lane & 1;
+      if (!keep) {   // as many beams have no children as keep no page: the r-th for the r-th
+        int r = __popc(~S.keeps[warp] & ((1u << lane) - 1)) + (warp ? __popc(~S.keeps[0]) : 0);
+        unsigned f = ~S.used[0];
+        int at = 0;
+        if (r >= __popc(f)) r -= __popc(f), f = ~S.used[1], at = 32;
+        while (r--) f &= f - 1;
+        from = at + __ffs(f) - 1;
+        if (parent >= 0) S.copied[__popc(S.copies[warp] & ((1u << lane) - 1)) + (warp ? __popc(S.copies[0]) : 0)] = tid;
+      }
+      S.page_of[tid] = from;
+    }
   }
   __syncthreads();
-  if (!last) return;
-  if (tid < p.W) tile[0][tid] = table[int64_t(F.page_of[tid]) * p.np_max + full];
-  __syncthreads();
-  if (tid < p.W) table[int64_t(tid) * p.np_max + full] = tile[0][tid];
+  // ---- copies: a plane (keys, or values, or the one of a packed cache) of a head
+  const int copies = part ? __popc(S.copies[0]) + __popc(S.copies[1]) : 0, each = p.Hk * p.planes;
+  for (int i = x; i < copies * each; i += gridDim.x) {
+    const int w = S.copied[i / each], h = i % each / p.planes, k = i % p.planes;
+    const int src = S.page[S.parent[w]], dst = S.page[S.page_of[w]], rows = S.rows[S.parent[w]];
+    if (src < 0 || src >= p.n_phys || dst < 0 || dst >= p.n_phys) {
+      if (i % each == 0 && tid == 0) flag_error(p.err, SPKV_DEVERR_PHYS);
+      continue;
+    }
+    const int bytes = p.row_bytes ? max(0, min(kPageTokens, rows)) * p.row_bytes : p.page_bytes;
+    const int64_t from = int64_t(h) * p.n_phys + src, to = int64_t(h) * p.n_phys + dst;
+    uint8_t* const pool = k ? p.pool[1] : p.pool[0];
+    const bool sums = k == 0 && p.ksum && tid * 16 < p.ksum_bytes;
+    uint4 v[kPieces], sum;
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int at = (j * kCopyThreads + tid) * 16;
+      if (at < bytes) v[j] = *reinterpret_cast<const uint4*>(pool + from * p.page_bytes + at);
+    }
+    if (sums) sum = *reinterpret_cast<const uint4*>(p.ksum + from * p.ksum_bytes + tid * 16);
+#pragma unroll
+    for (int j = 0; j < kPieces; ++j) {
+      const int at = (j * kCopyThreads + tid) * 16;
+      if (at < bytes) *reinterpret_cast<uint4*>(pool + to * p.page_bytes + at) = v[j];
+    }
+    if (sums) *reinterpret_cast<uint4*>(p.ksum + to * p.ksum_bytes + tid * 16) = sum;
+    if (p.page_cnt && i % each == 0 && tid == 0) p.page_cnt[dst] = rows;
+  }
+  // ---- complete pages
+  for (int c0 = x * kStrip; c0 < full; c0 += gridDim.x * kStrip) {
+    const int n = min(kStrip, full - c0);
+    for (int i = tid; i < W * kStrip; i += kCopyThreads)
+      if (i % kStrip < n) S.tile[i / kStrip][i % kStrip] = table[int64_t(i / kStrip) * p.np_max + c0 + i % kStrip];
+    __syncthreads();
+    for (int i = tid; i < W * kStrip; i += kCopyThreads) {
+      const int w = i / kStrip, from = S.parent[w];
+      if (i % kStrip < n && from >= 0 && from != w) table[int64_t(w) * p.np_max + c0 + i % kStrip] = S.tile[from][i % kStrip];
+    }
+    __syncthreads();
+  }
+  // ---- the column of part-filled pages
+  const bool last = before == static_cast<int>(gridDim.x) - 1;
+  if (last) p.arrived[b] = 0;
+  if (__syncthreads_or(last) && tid < W) table[int64_t(tid) * p.np_max + full] = S.page[S.page_of[tid]];
 }
 
 }  // namespace
@@ -860,10 +864,12 @@ int beam_reorder(spkv_cache_t c, const int32_t* parents, int B, int W, int32_t* 
   p.np_max = np_max;
   if (c->packed()) {
     p.pool[0] = c->pool4 ? c->pool4 : c->pool8;
+    p.planes = 1;
     p.page_bytes = c->pool4 ? 9216 : 16416;
   } else {
     p.pool[0] = static_cast<uint8_t*>(c->d.k_pool);
     p.pool[1] = static_cast<uint8_t*>(c->d.v_pool);
+    p.planes = 2;
     p.page_bytes = 16384;
     p.row_bytes = 256;
   }
@@ -873,8 +879,10 @@ int beam_reorder(spkv_cache_t c, const int32_t* parents, int B, int W, int32_t* 
   p.n_phys = c->d.n_phys_pages;
   p.arrived = c->beam_cnt;
   p.err = c->dev_err;
-  const int64_t strips = (np_max + spkv::kStrip - 1) / spkv::kStrip;
-  return spkv::launch_pdl(spkv::beam_reorder_kernel, dim3(static_cast<unsigned>(W * p.Hk + strips), B), dim3(256), 0,
+  // CTAs of a request: as many as there are copies or strips, as many an SM in all as it has room for
+  const int64_t work = std::max(int64_t(W - 1) * p.Hk * p.planes, int64_t(np_max + spkv::kStrip - 1) / spkv::kStrip);
+  const int64_t x = std::max(int64_t(1), std::min(work, int64_t(spkv::kCopyCtas) * c->sm_count / B));
+  return spkv::launch_pdl(spkv::beam_reorder_kernel, dim3(static_cast<unsigned>(x), B), dim3(spkv::kCopyThreads), 0,
                           static_cast<cudaStream_t>(stream), p) == cudaSuccess
              ? SPKV_OK
              : SPKV_ECUDA;
