@@ -122,6 +122,7 @@ cudaError_t init_kernel_attributes(const spkv_cache* c) {
     if ((e = attn_q4_init_attributes()) != cudaSuccess) return e;
   } else if (c->pool8) {
     if ((e = attn_q8_init_attributes()) != cudaSuccess) return e;
+    if ((e = append_q8_init_attributes()) != cudaSuccess) return e;
   } else {
     if ((e = attn_init_attributes()) != cudaSuccess) return e;
     if ((e = prefill_init_attributes()) != cudaSuccess) return e;
@@ -335,6 +336,7 @@ int paged_kv_append_rope(spkv_cache_t c, const void* k_new, int64_t k_stride, co
   p.n_rows = n_rows;
   p.B = B;
   p.Hq = Hq;
+  p.Hk = Hk;
   p.row_first = row_first;
   p.seq_len = seq_len;
   p.page_table = page_table;

@@ -184,7 +184,7 @@ struct Warp4 : Softmax<PACK> {
 
   // A page-head at shared address `at`, of whose 64 tokens `valid` exist.  The second half's scores do not
   // wait for the first's weights.
-  __device__ __forceinline__ void page(uint32_t at, int valid, int lane) {
+  __device__ __forceinline__ void page(uint32_t at, int valid, int lane, int) {
     if (valid <= 0) return;
     const uint32_t mine = at + lane * 16;
     const Half a{mine, mine + kQ4KScale, valid}, b{mine + 2048, mine + kQ4KScale + 8, valid - 32};
@@ -204,7 +204,7 @@ struct Warp4 : Softmax<PACK> {
 };
 
 template <int CG, bool PACK>
-struct Units4 : CtaShape<CG, PACK, PACK ? 7 : 6, PACK ? 28 : 12> {
+struct Units4 : CtaShape<CG, false, PACK ? 4 : 8 * CG, PACK ? 7 : 6, PACK ? 28 : 12> {
   static constexpr int kPage = kQ4Page;
   // Pages of a CTA where they are dealt, at least; of a part of a unit, at least; and of a part, at most, where the launch
   // alone lets CTAs take units.

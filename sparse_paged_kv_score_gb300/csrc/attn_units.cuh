@@ -1,12 +1,12 @@
 // What the attention kernels over packed caches (4-bit and 8-bit pools, one blob of bytes for a page of one kv head) share:
 // a warp's query fragments and running softmax, how the pages of all units are dealt to CTAs, brought to shared memory and
 // merged, and how such a kernel is launched.  A format is a struct F with
-//   CG, PACK        warps that share a page (one for every eight query heads); at most four query heads (see Softmax)
+//   CG, kByTokens   warps that share a page: each has some of its tokens, or eight of the query heads
 //   W, TEAMS, kThreads, NS, L, kCols, kDesc, kWindow, kCtasPerSm   CTA shape, see CtaShape
 //   kPage           bytes of a page-head
 //   kCtaPages, kPartPages, kUnitPages, kEndPages   how pages are dealt, see below
 //   Params          the kernel's parameters: a (AttnParams), pool, parts, part_pages
-//   Warp            a warp's arithmetic: Softmax<PACK> with page() and store()
+//   Warp            a warp's arithmetic: reset(), load_q(), page() and store() as Softmax and the formats have them
 //   score_factor(p, h), value_factor(p, h)   of kv head h: queries' scores to log2 units, values
 #pragma once
 #include <cuda_fp16.h>
@@ -79,6 +79,26 @@ struct State {
   float l[COLS];
 };
 
+// Dims 32 c .. 32 c + 31 (c = lane % 4) of query row g (of G rows of 128 bf16 at q0; zeros behind), and the power of two that
+// takes the row's largest magnitude into [2^13, 2^14) with its inverse; 1 for zero, infinity, NaN.
+__device__ __forceinline__ float scaled_row(const uint16_t* q0, int g, int G, int c, uint32_t (&w)[16], float& inv) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const uint4 v = g < G ? *reinterpret_cast<const uint4*>(q0 + g * kHeadDim + 32 * c + 8 * j) : make_uint4(0, 0, 0, 0);
+    w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
+  }
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < 16; ++j) m = max(m, max((w[j] & 0x7FFFu), (w[j] >> 16) & 0x7FFFu));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
+  m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
+  const int ex = static_cast<int>(m >> 7);
+  const int field = ex == 0 || ex == 255 ? 127 : min(253, 267 - ex);
+  inv = __uint_as_float(uint32_t(254 - field) << 23);
+  return __uint_as_float(uint32_t(field) << 23);
+}
+
+// A warp's running softmax for up to eight query heads of one unit: query column lane / 4 in the query
 // fragments, 2 (lane % 4) + {0, 1} in everything else.  PACK (at most four heads): columns 4..7 repeat
 // the heads of columns 0..3; the weights' hi parts go into the first half and the lo parts into the
 // second, so one MMA does both.
@@ -104,22 +124,9 @@ struct Softmax {
   // Query rows of one unit (G rows of 128 bf16 at q0), factor = gk / sqrt(128) log2 e.
   __device__ __forceinline__ void load_q(const uint16_t* q0, int G, float factor, int lane) {
     const int r = lane >> 2, c = lane & 3;
-    const int g = PACK ? (r & 3) : r;
     uint32_t w[16];   // dims 32 c .. 32 c + 31
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint4 v = g < G ? *reinterpret_cast<const uint4*>(q0 + g * kHeadDim + 32 * c + 8 * j) : make_uint4(0, 0, 0, 0);
-      w[4 * j] = v.x, w[4 * j + 1] = v.y, w[4 * j + 2] = v.z, w[4 * j + 3] = v.w;
-    }
-    uint32_t m = 0;
-#pragma unroll
-    for (int j = 0; j < 16; ++j) m = max(m, max((w[j] & 0x7FFFu), (w[j] >> 16) & 0x7FFFu));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 1));
-    m = max(m, __shfl_xor_sync(0xffffffffu, m, 2));
-    // power of two that takes the largest magnitude into [2^13, 2^14); 1 for zero, infinity, NaN
-    const int ex = static_cast<int>(m >> 7);
-    const int field = ex == 0 || ex == 255 ? 127 : min(253, 267 - ex);
-    const float f = __uint_as_float(uint32_t(field) << 23), inv = __uint_as_float(uint32_t(254 - field) << 23);
+    float inv;
+    const float f = scaled_row(q0, PACK ? (r & 3) : r, G, c, w, inv);
 #pragma unroll
     for (int ks = 0; ks < 8; ++ks) {
 #pragma unroll
@@ -188,16 +195,17 @@ __device__ __forceinline__ int page_of(const AttnParams& p, int u, int b, int i,
   return valid;
 }
 
-// CTA shape: four warps, of which CG (one for every eight query heads) share a page, and a ring of NS page
+// CTA shape: four warps, of which CG share a page, up to COLS query heads, and a ring of NS page
 // stages.  The barriers of the CTA's page j are number j % L of L, a multiple of the teams and of NS, so
 // that all of a barrier's phases are waited for by the same warps: a wait tells phases by their parity.
-template <int CG_, bool PACK_, int NS_, int L_, int CTAS = 3>
+template <int CG_, bool BY_TOKENS, int COLS, int NS_, int L_, int CTAS = 3>
 struct CtaShape {
   static constexpr int CG = CG_;
-  static constexpr bool PACK = PACK_;
+  static constexpr bool kByTokens = BY_TOKENS;
   static constexpr int W = 4, TEAMS = W / CG, kThreads = W * 32;
+  static constexpr int kStates = BY_TOKENS ? W : TEAMS;   // warps that share a page by heads share a state
   static constexpr int NS = NS_, L = L_;
-  static constexpr int kCols = PACK ? 4 : 8 * CG;
+  static constexpr int kCols = COLS;
   static constexpr int kDesc = kThreads;        // pages looked up at a time
   static constexpr int kWindow = 2 * kThreads;  // units among which they are looked up
   static constexpr int kCtasPerSm = CTAS;
@@ -208,7 +216,7 @@ template <class F>
 struct SmemUnits {
   using C = F;
   uint8_t stage[C::NS][C::kPage];
-  State<C::kCols> state[C::TEAMS];
+  State<C::kCols> state[C::kStates];
   union {
     uint2 desc[C::kDesc];    // place in the pool; valid tokens, unit of the window << 8
     int scan[C::kThreads];   // until the first look-up: first page of each thread's units
@@ -253,7 +261,7 @@ __device__ __forceinline__ void attend_units(const typename F::Params& pf) {
   SmemUnits<F>& S = *reinterpret_cast<SmemUnits<F>*>(smem_raw);
   const AttnParams& p = pf.a;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int team = warp / C::CG, c8 = 8 * (warp % C::CG);
+  const int team = warp / C::CG, piece = warp % C::CG, c8 = C::kByTokens ? 0 : 8 * piece;
   const int U = p.B * p.Hk, cta = blockIdx.x;
   if (tid < L) {
     mbar_init(&S.full[tid], 1);
@@ -449,7 +457,7 @@ __device__ __forceinline__ void attend_units(const typename F::Params& pf) {
         const int j = j0 + i, s = j % NS;
         ok = __all_sync(0xffffffffu, mbar_wait(&S.full[j % L], (j / L) & 1, p.wait_ns));
         if (!ok) break;
-        w.page(smem_u32(S.stage[s]), S.desc[i].y & 255, lane);
+        w.page(smem_u32(S.stage[s]), S.desc[i].y & 255, lane, piece);
         __syncwarp();
         if (lane == 0 && i + NS < cnt) {
           bool free = true;
@@ -465,8 +473,8 @@ __device__ __forceinline__ void attend_units(const typename F::Params& pf) {
       if (!ok && lane == 0) flag_error(p.err, SPKV_DEVERR_TIMEOUT);
       kb = ke;
       if (x + ke < min(e, x1)) break;   // it goes on with the next descriptors
-      // ---- its end: the teams' states merged, a warp taking a query head at a time
-      w.store(S.state[team], c8, lane);
+      // ---- its end: the warps' states merged, a warp taking a query head at a time
+      w.store(S.state[C::kByTokens ? warp : team], c8, lane);
       w.reset();   // nothing of it is kept over the merges
       const int gap = C::kEndPages * u;
       const bool whole = f >= x0 && e <= x1;   // a unit is in the window or out of it
@@ -477,9 +485,9 @@ __device__ __forceinline__ void attend_units(const typename F::Params& pf) {
         float M = -CUDART_INF_F, sum = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int t = 0; t < TEAMS; ++t) M = fmaxf(M, S.state[t].m[g]);
+        for (int t = 0; t < C::kStates; ++t) M = fmaxf(M, S.state[t].m[g]);
 #pragma unroll
-        for (int t = 0; t < TEAMS; ++t) {
+        for (int t = 0; t < C::kStates; ++t) {
           const float m = S.state[t].m[g], l = S.state[t].l[g];
           const float4 o = *reinterpret_cast<const float4*>(&S.state[t].o[g][4 * lane]);
           // no token: left out (a NaN sum is not)

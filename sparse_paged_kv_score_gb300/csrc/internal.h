@@ -188,6 +188,7 @@ struct AppendRopeParams {
   int64_t k_stride, v_stride, q_stride;
   uint16_t* q_out;               // [n_rows][Hq][128]
   int n_rows, B, Hq, G;          // G = 0 without queries
+  int Hk, heads;                 // kv heads, of a CTA (the 8-bit form's; set by the launch)
   const int32_t* row_first;      // [B + 1] or null: row i is request i's
   const int32_t* seq_len;
   const int32_t* page_table;
@@ -223,6 +224,7 @@ cudaError_t launch_unpack_q8(const spkv_cache* c, const int32_t* pages, int n_pa
                              cudaStream_t st);
 cudaError_t launch_attn_q8(const spkv_cache* c, const AttnParams& a, cudaStream_t st);
 cudaError_t attn_q8_init_attributes();
+cudaError_t append_q8_init_attributes();
 cudaError_t launch_append(const spkv_cache* c, const int32_t* phys, const int32_t* tok, const void* k_new,
                           const void* v_new, int n_rows, cudaStream_t st);
 // The fused decode append's pointers (k_new, v_new: bf16 [B][Hk][128] as 32-bit words).

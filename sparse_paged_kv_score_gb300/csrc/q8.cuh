@@ -43,16 +43,17 @@ __device__ __forceinline__ uint32_t q8_scale(uint32_t a) {
   if (a >= 0x7F800000u) return kQ8NaN;
   return static_cast<uint32_t>(max(static_cast<int>(a >> 23) - 6, 1)) << 23;
 }
-// 1 / s of a scale; 0 for 0 and NaN (their codes are then 0).
+// 1 / s of a scale; 0 for 0 and NaN.
 __device__ __forceinline__ float q8_inverse(uint32_t s) {
   return s == 0 || s >= 0x7F800000u ? 0.f : __uint_as_float((254u << 23) - s);
 }
-// Byte of x: the product is exact but where it is below 2^-149, and rounded down there as the floor wants it.
-__device__ __forceinline__ uint32_t q8_byte(float x, float inverse) {
-  return static_cast<uint32_t>(__float2int_rd(__fmul_rd(x, inverse)) + 128) & 0xFFu;
-}
+// Bytes of four values under a scale's inverse: floor(x / s) + 128, from one fused product and sum rounded down (so that a
+// negative number too small for fp32 gives -1).  1.5 * 2^23: the sum's last bits are the integer's.
 __device__ __forceinline__ uint32_t q8_bytes(float4 x, float inverse) {
-  return q8_byte(x.x, inverse) | q8_byte(x.y, inverse) << 8 | q8_byte(x.z, inverse) << 16 | q8_byte(x.w, inverse) << 24;
+  constexpr float kMagic = 12582912.f + 128.f;
+  const uint32_t a = __float_as_uint(__fmaf_rd(x.x, inverse, kMagic)), b = __float_as_uint(__fmaf_rd(x.y, inverse, kMagic));
+  const uint32_t c = __float_as_uint(__fmaf_rd(x.z, inverse, kMagic)), d = __float_as_uint(__fmaf_rd(x.w, inverse, kMagic));
+  return __byte_perm(__byte_perm(a, b, 0x0040), __byte_perm(c, d, 0x0040), 0x5410);
 }
 // Powers of two by which codes under scale `was` shrink under scale `is` >= was (8 leaves only their sign).
 __device__ __forceinline__ int q8_shift(uint32_t was, uint32_t is) {
