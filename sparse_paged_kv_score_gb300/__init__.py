@@ -74,9 +74,11 @@ def _stream(stream) -> int:
 
 
 def _t(x: torch.Tensor, dtype, name: str, shape=None) -> int:
-    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.is_cuda and x.is_contiguous()
-            and (shape is None or x.shape == shape)):
-        return x.data_ptr()
+    try:   # the usual case, on every call: few attributes, each looked up once
+        if x.dtype is dtype and x.is_cuda and x.is_contiguous() and (shape is None or x.shape == shape):
+            return x.data_ptr()
+    except AttributeError:
+        pass
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if x.dtype != dtype:
@@ -237,9 +239,11 @@ def _same_device(device, **tensors) -> None:
 
 def _at(x: torch.Tensor, dtype, name: str, shape, index: int) -> int:
     """_t of a tensor on CUDA device ``index``."""
-    if (isinstance(x, torch.Tensor) and x.dtype is dtype and x.get_device() == index and x.is_contiguous()
-            and x.shape == shape and index >= 0):
-        return x.data_ptr()
+    try:
+        if x.dtype is dtype and x.get_device() == index and x.is_contiguous() and x.shape == shape and index >= 0:
+            return x.data_ptr()
+    except AttributeError:
+        pass
     at = _t(x, dtype, name, shape)
     _same_device(torch.device("cuda", index), **{name: x})
     return at
@@ -367,30 +371,32 @@ def beam_select(cache: PagedKVCache, plan: BeamPlan, logits, cum, tokens, parent
     """The K best continuations of each request's W beams: logits fp32, bf16 or fp16 [B][W][V] (rows may lie apart, evenly),
     cum fp32 [B][W] the beams' scores so far (-inf: none); tokens, parents int32 and scores fp32 [B][K], best first, -1, -1,
     -inf where there are fewer."""
+    dev = cache.tensors[0].get_device()
     if not isinstance(logits, torch.Tensor):
         raise TypeError("logits: expected a torch.Tensor")
     kind = _LOGITS.get(logits.dtype)
     if kind is None:
         raise TypeError(f"logits: expected float32, bfloat16 or float16, got {logits.dtype}")
-    dev = cache.tensors[0].get_device()
     if logits.get_device() != dev or dev < 0:
         raise ValueError("logits: must be a CUDA tensor on the cache's device")
     if logits.dim() != 3:
         raise ValueError("logits: expected [B][W][V]")
     B, W, V = logits.shape
-    sb, sw, one = logits.stride()
-    row = sw if W > 1 else sb if B > 1 else V
-    if (one != 1 and V > 1) or (B > 1 and W > 1 and sb != W * sw):
-        raise ValueError("logits: rows must be contiguous and evenly apart")
-    K = tokens.shape[1] if tokens.dim() == 2 else 0
+    row = V
+    if not logits.is_contiguous():
+        sb, sw, one = logits.stride()
+        row = sw if W > 1 else sb if B > 1 else V
+        if (one != 1 and V > 1) or (B > 1 and W > 1 and sb != W * sw):
+            raise ValueError("logits: rows must be contiguous and evenly apart")
+    best = (B, tokens.shape[-1])
     c = _at(cum, torch.float32, "cum", (B, W), dev)
-    t, p = _at(tokens, torch.int32, "tokens", (B, K), dev), _at(parents, torch.int32, "parents", (B, K), dev)
-    s = _at(scores, torch.float32, "scores", (B, K), dev)
+    t, p = _at(tokens, torch.int32, "tokens", best, dev), _at(parents, torch.int32, "parents", best, dev)
+    s = _at(scores, torch.float32, "scores", best, dev)
     if torch._C._cuda_getDevice() != dev:
         with torch.cuda.device(dev):
             return beam_select(cache, plan, logits, cum, tokens, parents, scores, stream)
     st = torch._C._cuda_getCurrentRawStream(dev) if stream is None else _stream(stream)
-    check("beam_select", load().beam_select(cache.handle, plan.handle, logits.data_ptr(), kind, row, B, W, V, c, K, t, p, s, st))
+    check("beam_select", load().beam_select(cache.handle, plan.handle, logits.data_ptr(), kind, row, B, W, V, c, best[1], t, p, s, st))
 
 
 def beam_reorder(cache: PagedKVCache, parents, page_table, seq_len, stream=None):
