@@ -344,7 +344,7 @@ __device__ __forceinline__ void ask(uint8_t* stage, const uint8_t* from, const u
   auto copy = [&](int x) {   // 16 bytes from x on, zeros behind the row
     const int64_t left = end - (at + x);
     const int n = left >= 16 ? 16 : left > 0 ? static_cast<int>(left) : 0;
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + x), "l"(n ? at + x : from - off + 16), "r"(n) : "memory");
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + x), "l"(n ? at + x : begin - (reinterpret_cast<uintptr_t>(begin) & 15)), "r"(n) : "memory");
   };
   const bool head = at < begin;   // the row begins inside its first 16 bytes
 #pragma unroll
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_consta
       collect(i);
     }
     __syncthreads();
-    if (S.left[1] > 2 * most) {
+    if (S.left[1] > min(2 * most, kListed)) {
       t = threshold(S, lines, p.K, most, turn, lo, hi, mine);
       if (tid == 0) S.left[1] = 0;
       __syncthreads();

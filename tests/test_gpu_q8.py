@@ -231,6 +231,17 @@ def test_append_many_rows(lens):
     b.check(b.expect())
 
 
+@pytest.mark.parametrize("Hq,Hk", [(40, 8), (6, 6), (22, 2), (16, 1), (3, 3)])
+@pytest.mark.parametrize("pad,fused,axes", [(0, False, 1), (37, True, 3)])
+def test_append_many_rows_heads(Hq, Hk, pad, fused, axes):
+    """Query heads that slices do not divide, kv heads that CTAs do not, rows behind the last request's, strided rows."""
+    n = 2700 // Hk + 100
+    b = Batch([5, 0, 63], [n // 2, 17, n // 3], Hq, Hk, seed=19, pad=pad, fused=fused, axes=axes, sum16=bool(pad))
+    b.call()
+    assert spkv.get_device_error(b.cache) == (0, 0)
+    b.check(b.expect())
+
+
 @pytest.mark.parametrize("cuts", [[1] * 70, [3] * 23 + [1], [16, 16, 16, 22], [33, 37], [69, 1]])
 def test_append_in_any_pieces(cuts):
     """However a prompt is cut into calls, the cache holds the same bytes: floors compose."""

@@ -120,6 +120,42 @@ print(json.dumps([prepared, refused, runs, bad, other]))
     assert other == [-6, -6]
 
 
+@pytest.mark.parametrize("sms", [[152, 148], [90, 85], [40, 20, 8, 1]])
+def test_launch_choices(fake, sms):
+    """Attention: where CTAs take parts of units (mode 2) the grid is whole units; never more CTAs than have room at once.
+    Appends: a CTA for every window and kv head, or slice of them."""
+    program = HANDLE + """
+import re
+got, rows = [], []
+for sms in SMS:
+    f.rt.fake_sms(sms)
+    for Hk in (1, 8):
+        h = handle8(Hk)
+        f.events()
+        for B in (1, 2, 13, 32, 61, 128, 256, 500):
+            for n in (1, 3, 4, 17, 65, 129, 700):
+                for G in (1, 5, 16):
+                    assert f.lib.sparse_decode_attn(h, P, B, G * Hk, P, 9, P, P, n, P, P, P, None) == 0
+                    (e,) = f.events()
+                    heads, mode, grid = map(int, re.search(r"attn_q8_kernelILi(\\d+)E\\S*ModeE(\\d)\\S* (\\d+)$", e).groups())
+                    got.append([sms, B * Hk, G, heads, mode, grid])
+        for n in (1, 5, 200, 1000, 30000):
+            assert f.lib.paged_kv_append_rope(h, P, 128 * Hk, P, 128 * Hk, n, n, None, P, P, 4, None, None, 0, 0, None, None) == 0
+            (e,) = f.events()
+            rows.append([sms, Hk, n, "blocks" in e, int(e.split()[-1])])
+print(json.dumps([got, rows]))
+""".replace("SMS", repr(sms))
+    got, rows = json.loads(fake_cuda.run(fake, program))
+    room = {4: 3, 8: 2, 16: 2}      # CTAs of an SM
+    for m, U, G, heads, mode, grid in got:
+        assert heads == (4 if G <= 4 else 8 if G <= 8 else 16)
+        assert 1 <= grid <= room[heads] * m, (m, U, G, mode, grid)
+        assert mode != 2 or grid % U == 0
+    for m, Hk, n, blocks, grid in rows:
+        window = 16 if blocks else 1 if (n + 3) // 4 * Hk < m else 4
+        assert grid == (n + window - 1) // window and (blocks or grid * window >= n)
+
+
 def test_reference_pins():
     """The tests' own form of the format: what spkv.h says of it."""
     assert sorted(np.concatenate([ref.KC, ref.VC]).flatten()) == list(range(16384))
