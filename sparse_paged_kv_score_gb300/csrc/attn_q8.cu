@@ -370,7 +370,11 @@ struct Warp8Wide {
   }
 };
 
-// HEADS: query heads at most, 4, 8 or 16.
+// HEADS: query heads at most, 4, 8 or 16.  Two warps share a page by tokens: a page is half as long in its stage, and few long
+// lists end sooner (us, 1 / 2 / 4 warps a page: one request of 129 pages x 8 heads 12.6 / 11.9 / 12.9, 256 units of 65 pages 51.1 /
+// 51.3 / 52.9).  Up to eight heads could be rows of the wide form too, but half of its first product would be zeros; sixteen
+// as columns of two warps, each unpacking every page, took 71 us for 256 units of 65 pages, the wide form takes 60.
+// Three CTAs an SM where registers and stages allow it; the wide form with three (168 registers, fewer stages) took 67 to 76.
 template <int HEADS>
 struct Shape8;
 template <>
@@ -389,12 +393,19 @@ struct Shape8<16> : CtaShape<2, true, 16, 4, 4, 2> {
 template <int HEADS>
 struct Units8 : Shape8<HEADS> {
   static constexpr int kPage = kQ8Page;
+  // As the 4-bit attention's, with parts of two pages (2 units of 17 pages, parts of 2 / 3 / 4 / 6: 6.4 / 7.0 / 6.9 / 7.6 us); 8, 4, 2
+  // places at a unit's end: 61 lists of up to 129 pages 26.0, 26.6, 27.9 us, the rest alike.
   static constexpr int kCtaPages = 8, kPartPages = 2, kUnitPages = 16, kEndPages = 8;
   using Params = AttnQ8Params;
   static __device__ __forceinline__ float score_factor(const Params& p, int) { return p.a.scale_log2; }
   static __device__ __forceinline__ float value_factor(const Params&, int) { return 1.f; }
 };
 
+// Measured (GB300, from a replayed graph): 256 units of 65 pages, 4 heads 50.1 us = 275 MB at 5.5 TB/s (0.82 of the copy rate);
+// 8 heads 49.0, 16 heads 60.2; 61 lists of up to 129 pages, 16 heads 26 us; 2 of 17 pages 6.4.  Times of 96 to 300 units lie on
+// a line of 6.37 TB/s (0.95 of the copy rate) behind 8 us: lengths, lists, page table and first page read one after the
+// other, and the CTAs' ends.  With 9 to 16 heads a page's 1240 instructions in two warps are what bounds it, in chains that two
+// warps a scheduler (255 registers) do not hide: they issue in a third of the slots.
 enum Mode { kDealt, kEither, kByUnit };
 
 template <int HEADS, Mode MODE>

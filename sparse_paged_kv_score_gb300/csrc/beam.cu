@@ -440,26 +440,26 @@ __global__ void __launch_bounds__(kGroupThreads, kCtasPerSm) beam_groups_kernel(
   struct Place {
     int row, g;
   };
-  // moves to the first group from x on of a beam that has not ended (one that has is not read, nor what would be written of it)
   auto forward = [&](Place x) {
     x.row += step_row;
     x.g += step_g;
     if (x.g >= p.groups) x.g -= p.groups, ++x.row;
     return x;
   };
-  auto live = [&](Place x) {
-    while (x.row < p.rows && p.cum[x.row] == -CUDART_INF_F) x = forward(x);
-    return x;
-  };
+  auto cum_of = [&](Place x) { return x.row < p.rows ? p.cum[x.row] : 0.f; };
   const int first = blockIdx.x * (kGroupThreads / 32) + warp;
-  Place next = live({first / p.groups, first % p.groups});   // to be asked for
+  Place next{first / p.groups, first % p.groups};   // to be asked for, with its beam's score (not waited for until then)
+  float cum = cum_of(next);
   Place queue[kStages - 1];
   auto ask_next = [&](int s) {
+    // a beam that has ended is not read, nor what would be written of it
+    while (cum == -CUDART_INF_F) next = forward(next), cum = cum_of(next);
     const Place x = next;
     if (x.row < p.rows) {
       const uint8_t* const r0 = p.logits + x.row * p.row_bytes;
       ask<T>(mine + s * kStage, r0 + int64_t(x.g) * kGroupBytes, r0, r0 + int64_t(p.V) * sizeof(T), lane);
-      next = live(forward(x));
+      next = forward(x);
+      cum = cum_of(next);
     }
     asm volatile("cp.async.commit_group;" ::: "memory");
     return x;
