@@ -276,6 +276,14 @@ __device__ int select_best(SmemBeam& S, int n, int K, F make) {
   return want;
 }
 
+// An element, or a line's maximum, its beam, and an element's place.
+struct Item {
+  float x;
+  int w, place;
+};
+constexpr int kLineBits = 20, kLineMask = (1 << kLineBits) - 1;
+static_assert(kMaxGroups * kLines <= 1 << kLineBits && kMaxBeams <= 1 << (31 - kLineBits) && kLines == 32, "a line and its beam in an int");
+
 // Where item i of a request's groups, of the lines of listed groups and of the elements of listed lines lies, and its key.
 template <typename T>
 struct Items {
@@ -287,31 +295,40 @@ struct Items {
   __device__ __forceinline__ Key group(int g) const {
     return key_of(p.group[first() + g].x, off[g / p.groups]);
   }
-  // line: group * kLines + its line of the group
-  __device__ __forceinline__ Key line(int x) const {
-    return key_of(p.line_max[first() * kLines + x], off[x / kLines / p.groups]);
-  }
+  // Groups and lines are listed with their beam: line = beam << kLineBits | group * kLines + its line of the group.
+  __device__ __forceinline__ int listed(int g) const { return (g / p.groups) << (kLineBits - 5) | g; }
+  __device__ __forceinline__ Item line(int x) const { return {p.line_max[first() * kLines + (x & kLineMask)], x >> kLineBits, 0}; }
   // element e of line x; place: beam * V + token
-  __device__ __forceinline__ Key element(int x, int e, int& place) const {
-    const int w = x / kLines / p.groups, token = (x - w * p.groups * kLines) * kEach + e;
-    place = w * p.V + token;
-    if (token >= p.V) return 0;
-    return key_of(Traits<T>::one(reinterpret_cast<const T*>(p.logits + (int64_t(b) * p.W + w) * p.row_bytes) + token), off[w]);
+  __device__ __forceinline__ Item element(int x, int e) const {
+    const int w = x >> kLineBits, token = ((x & kLineMask) - w * p.groups * kLines) * kEach + e;
+    if (token >= p.V) return {-CUDART_INF_F, w, w * p.V + token};
+    return {Traits<T>::one(reinterpret_cast<const T*>(p.logits + (int64_t(b) * p.W + w) * p.row_bytes) + token), w, w * p.V + token};
   }
+  __device__ __forceinline__ Key key(const Item& i) const { return key_of(i.x, off[i.w]); }
 };
 
-// The K best of n elements in S.best, S.place to the outputs, -1, -1, -infinity behind them: a warp counts what is ahead of
-// an element.
+// The K best of n elements in S.best, S.place to the outputs, -1, -1, -infinity behind them: four lanes count what is ahead
+// of an element.
 __device__ __forceinline__ void write_best(SmemBeam& S, const BeamParams& p, int b, int n) {
   const int64_t o = int64_t(b) * p.K;
-  const int lane = threadIdx.x & 31;
-  for (int i = threadIdx.x >> 5; i < n; i += kWarps) {
-    const Key k = S.best[i];
-    const int place = S.place[i];
-    int at = 0;
-    for (int j = lane; j < n; j += 32) at += S.best[j] > k || (S.best[j] == k && S.place[j] < place);
-    at = __reduce_add_sync(0xffffffffu, at);
-    if (lane || at >= p.K) continue;
+  for (int i = threadIdx.x >> 2; i - (threadIdx.x >> 2 & 7) < n; i += kThreads / 4) {   // by warps
+    const Key k = i < n ? S.best[i] : ~0ull;
+    const uint32_t half = static_cast<uint32_t>(k >> 32);
+    int at = 0, same = 0;   // elements ahead by their half keys, with the same half (itself one of them)
+    for (int j = threadIdx.x & 3; j < n; j += 4) {
+      const uint32_t other = S.best[j] >> 32;
+      at += other > half;
+      same += other == half;
+    }
+    const int place = i < n ? S.place[i] : 0;
+    if (__any_sync(0xffffffffu, i < n && same > (static_cast<int>(threadIdx.x & 3) == (i & 3))))
+      for (int j = threadIdx.x & 3; j < n; j += 4) {
+        const Key o = S.best[j];
+        at += o >> 32 == half && (o > k || (o == k && S.place[j] < place));
+      }
+    at += __shfl_xor_sync(0xffffffffu, at, 1);
+    at += __shfl_xor_sync(0xffffffffu, at, 2);
+    if ((threadIdx.x & 3) || i >= n || at >= p.K) continue;
     const int w = place / p.V;
     p.tokens[o + at] = place - w * p.V;
     p.parents[o + at] = w;
@@ -487,7 +504,8 @@ __global__ void __launch_bounds__(kGroupThreads, kCtasPerSm) beam_groups_kernel(
 
 // A CTA a request: its K best from its groups' maxima and sums.
 // Bound by latency: three searches, each reads what the one before has found.  4 beams x 32000 with the first kernel 6.5 us
-// from a replayed graph, one row 6.0; 64-bit keys and scores in it took 12.1.
+// from a replayed graph, one row 6.0; 64-bit keys and scores in it took 12.1.  4 requests of 64 beams x 128256 fp32, K = 128, 54 us (19.7 for the bytes),
+// by the instructions of one CTA a request: 59 with a division for each line and element and whole keys compared at the end.
 template <typename T>
 __global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_constant__ BeamParams p) {
   extern __shared__ __align__(16) uint8_t smem_raw[];
@@ -546,9 +564,10 @@ __global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_consta
   for (int i = tid; i < n; i += kThreads) {
     if (S.key[i] < t) continue;
     const int x = atomicAdd(&S.left[0], 1);
-    if (x < kListed) S.groups[x] = i;
+    if (x < kListed) S.groups[x] = it.listed(i);
   }
   __syncthreads();
+  auto element_of = [&](int i) { return it.element(S.lines[i / it.kEach], i % it.kEach); };
   auto line_of = [&](int i) { return S.groups[i / kLines] * kLines + i % kLines; };
   bool fits = S.left[0] <= kListed;
   if (fits) {
@@ -562,7 +581,7 @@ __global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_consta
       if (at < kListed) S.lines[at] = line_of(i);
     };
     for (int i = tid; i < lines; i += kThreads) {
-      keep(i, it.line(line_of(i)));
+      keep(i, it.key(it.line(line_of(i))));
       collect(i);
     }
     __syncthreads();
@@ -578,11 +597,11 @@ __global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_consta
   if (fits) {
     // ---- their elements that reach it
     for (int i = tid; i < S.left[1] * it.kEach; i += kThreads) {
-      int place;
-      const Key k = it.element(S.lines[i / it.kEach], i % it.kEach, place);
+      const Item x = element_of(i);
+      const Key k = it.key(x);
       if (k >> 32 < t) continue;
       const int at = atomicAdd(&S.left[2], 1);
-      if (at < kElements) S.best[at] = k, S.place[at] = place;
+      if (at < kElements) S.best[at] = k, S.place[at] = x.place;
     }
     __syncthreads();
     if (S.left[2] <= kElements) return write_best(S, p, b, S.left[2]);
@@ -590,16 +609,16 @@ __global__ void __launch_bounds__(kThreads) beam_best_kernel(const __grid_consta
   // ---- too many alike: exactly K groups, of their lines exactly K, of those lines' elements
   __syncthreads();
   const int ng = select_best(S, n, p.K, [&](int i) { return it.group(i); });
-  if (tid < ng) S.groups[tid] = S.sorted[tid];
+  if (tid < ng) S.groups[tid] = it.listed(S.sorted[tid]);
   __syncthreads();
-  const int nl = select_best(S, ng * kLines, p.K, [&](int i) { return it.line(line_of(i)); });
+  const int nl = select_best(S, ng * kLines, p.K, [&](int i) { return it.key(it.line(line_of(i))); });
   if (tid < nl) S.lines[tid] = line_of(S.sorted[tid]);
   __syncthreads();
-  int place;
-  const int ne = select_best(S, nl * it.kEach, p.K, [&](int i) { return it.element(S.lines[i / it.kEach], i % it.kEach, place); });
+  const int ne = select_best(S, nl * it.kEach, p.K, [&](int i) { return it.key(element_of(i)); });
   if (tid < ne) {
-    S.best[tid] = it.element(S.lines[S.sorted[tid] / it.kEach], S.sorted[tid] % it.kEach, place);
-    S.place[tid] = place;
+    const Item x = element_of(S.sorted[tid]);
+    S.best[tid] = it.key(x);
+    S.place[tid] = x.place;
   }
   __syncthreads();
   write_best(S, p, b, ne);
