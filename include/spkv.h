@@ -284,7 +284,7 @@ int beam_plan_destroy(spkv_beam_plan_t plan);
 /* The K best continuations of each request:
  *   score[w][v] = cum[b][w] + (logits[b W + w][v] - log sum_u exp(logits[b W + w][u]))
  * over beams w and tokens v, best first; of equal scores the lower beam, then the lower token goes first.  Sums are formed in
- * fp32 over 4 KiB of a row, then in 48 bits, as are scores.
+ * fp32, over each 4 KiB of a row, then over those; scores in 48 bits.
  *   logits  : device, rows row_stride elements apart, each [V] of `type`; aligned to its elements
  *   cum     : device fp32 [B][W], the beams' scores so far; -infinity: a beam that has ended or does not exist yet (its
  *             logits are not read, it has no candidates)

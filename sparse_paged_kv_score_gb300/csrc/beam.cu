@@ -10,7 +10,8 @@
 // K groups, K of their lines and K elements, of equal ones the first each time (an element among the K best lies in a line
 // whose maximum is among the K best of the lines', as each line ahead of it holds an element ahead of it, and likewise a line
 // in its group; groups, lines and elements are numbered by beam and token).
-// Sums are fp32 within 4 KiB, then 48 bits, as scores are: those of different beams may lie close together.
+// Sums are fp32 within 4 KiB, and over a row's groups, a 32nd of them to a lane.  Scores have 48 bits: those of different beams
+// may lie close together.
 //
 // beam_reorder.  Complete pages are shared, so a child takes its parent's table entries; of the part-filled page a parent's
 // first child keeps the parent's own, and each other child gets the page of a beam without children, with the parent's rows
@@ -116,10 +117,9 @@ __device__ __forceinline__ void add_exps(float& s0, float& s1, uint4 v, float c)
     }
   }
 }
-// exp(x - m) for a maximum m of 2^126 or more, whose product with log2e may be no fp32 number: what is not m is too far away
-// to count.  NaN for NaN and for m = infinity, 0 for m = -infinity.
+// exp(x - m) for any maximum m: NaN for NaN and for m = infinity, 0 for m = -infinity.
 __device__ __forceinline__ float far_exp(float x, float m) {
-  return x != x || m == CUDART_INF_F ? CUDART_NAN_F : x == m && m > -CUDART_INF_F ? 1.f : 0.f;
+  return x != x || m == CUDART_INF_F ? CUDART_NAN_F : m == -CUDART_INF_F ? 0.f : ex2((x - m) * kLog2e);
 }
 template <typename T>
 __device__ __forceinline__ float far_exps(uint4 v, float m) {
@@ -430,7 +430,7 @@ __device__ __forceinline__ void look_at_group(const BeamParams& p, const uint4 (
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   float s = 0.f;
-  if (fabsf(top) < 0x1p126f) {
+  if (fabsf(top) < 0x1p24f) {   // c is off by 1 at most: so are the exponents, which the last factor puts right
     const float c = __fmul_rn(top, kLog2e);
     float s0 = 0.f, s1 = 0.f;
 #pragma unroll
@@ -879,7 +879,7 @@ int beam_select(spkv_cache_t c, spkv_beam_plan_t plan, const void* logits, int t
 int beam_reorder(spkv_cache_t c, const int32_t* parents, int B, int W, int32_t* page_table, int np_max, const int32_t* seq_len,
                  void* stream) {
   if (!c || B < 0 || W <= 0) return SPKV_EINVAL;
-  if (W > kMaxBeams || c->d.n_kv_heads > 65535) return SPKV_EUNSUPPORTED;
+  if (W > kMaxBeams) return SPKV_EUNSUPPORTED;
   if (int64_t(B) * W * c->d.n_kv_heads > c->max_units) return SPKV_EINVAL;
   if (B == 0) return SPKV_OK;
   if (!parents || !page_table || np_max <= 0 || !seq_len || !on_device(c->device)) return SPKV_EINVAL;

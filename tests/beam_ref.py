@@ -31,10 +31,12 @@ def best(s, K):
 
 def lse_error(V):
     """Bound on the kernel's error of a row's log of the sum of exponentials: a term exp(x - m) is off by its argument's two
-    roundings, 2^-23 |x - m|, and by exp2's 2^-22; the terms' share-weighted mean of |x - m| is at most log V (the entropy of
-    the shares); 64 terms to a lane and five steps over lanes, half a step of 2^-23 each, one rounded exponential for each
-    4 KiB, and the rest in 64 bits."""
-    return np.log(V + 1) * 2.0 ** -23 + 2.0 ** -22 + 69 * 2.0 ** -24 + 2.0 ** -22
+    roundings, 2^-23 |x - m| (2^-24 more where m nears 2^24), and by exp2's 2^-22; the terms' share-weighted mean of |x - m| is at most log V (the entropy of
+    the shares); 64 terms to a lane and five steps over lanes, half a step of 2^-23 each.  Then one term for each 4 KiB (at
+    least 1024 tokens): an exponential of a rounded difference (2^-24 of it, again log V in the mean; the exponential 2^-22),
+    a product, a 32nd of the terms to a lane and five steps over lanes.  The logarithm of the sum is off by 2^-22 at most."""
+    terms = -(-V // 1024)
+    return np.log(V + 1) * 1.5 * 2.0 ** -23 + 3 * 2.0 ** -22 + (1 + 69 + 1 + -(-terms // 32) + 5) * 2.0 ** -24
 
 
 def check_best(x, cum, K, tokens, parents, scores):

@@ -116,6 +116,20 @@ def test_select_orders(order):
     s.check()
 
 
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dtype,e", [(t, e) for t, es in ((torch.float32, (10, 20, 23, 24, 25, 29, 30, 31, 32, 40, 64, 100, 125, 126, 127)),
+                                                           (torch.bfloat16, (7, 15, 23, 24, 30, 31, 33, 64, 126, 127)),
+                                                           (torch.float16, (7, 11, 15))) for e in es])
+def test_select_sizes(dtype, e, sign):
+    """Logits of magnitude 2^e, some of them steps of their type apart, and far smaller ones."""
+    V, step = 5000, torch.finfo(dtype).eps * 2.0 ** e
+    x = 2.0 ** e + step * torch.randint(0, 9, (2, 3, V), generator=torch.Generator().manual_seed(e)).double()
+    x[:, :, ::7] = torch.randn(2, 3, x[:, :, ::7].shape[2], dtype=torch.float64) if sign > 0 else 1.5 * 2.0 ** e
+    s = Select((sign * x).to(dtype), cums(2, 3, e), 12)
+    s.call()
+    s.check()
+
+
 @pytest.mark.parametrize("dtype", TYPES)
 def test_select_masks(dtype):
     """-infinity and the type's lowest value as masks; rows with nothing left, few tokens left; beams that ended."""
