@@ -215,6 +215,10 @@ struct Units4 : CtaShape<CG, false, PACK ? 4 : 8 * CG, PACK ? 7 : 6, PACK ? 28 :
   // 26.3 / 26.9, 256 of 65 37.2 / 37.5 / 37.3 / 37.2, a step with 128 of 65 38.3 / 40.3 / 38.8 / 37.9.
   static constexpr int kEndPages = 8;
   using Params = AttnQ4Params;
+  // Through a reference the kernels by unit spill (16 bytes a thread for 5 to 8 heads).  Reference / copy (us): one unit of 17 pages,
+  // 8 heads 8.35 / 7.85, 16 heads 11.4 / 10.3; 64 of 33, 8 heads 14.8 / 14.2; 64 of 129, 8 heads 26.3 / 26.2, 5 heads 25.7 /
+  // 25.5; 256 of 65, 4 heads 36.6 / 36.6.
+  using Held = const AttnQ4Params;
   using Warp = Warp4<PACK>;
   static __device__ __forceinline__ float score_factor(const Params& p, int h) { return p.a.scale_log2 * p.k_scale[h]; }
   static __device__ __forceinline__ float value_factor(const Params& p, int h) { return p.v_scale[h]; }

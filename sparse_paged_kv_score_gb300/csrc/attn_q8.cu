@@ -397,6 +397,7 @@ struct Units8 : Shape8<HEADS> {
   // places at a unit's end: 61 lists of up to 129 pages 26.0, 26.6, 27.9 us, the rest alike.
   static constexpr int kCtaPages = 8, kPartPages = 2, kUnitPages = 16, kEndPages = 8;
   using Params = AttnQ8Params;
+  using Held = const AttnQ8Params&;   // (a copy: 64 units of 129 pages, 16 heads 37.0 us for 36.5; 4 and 8 heads within 0.2)
   static __device__ __forceinline__ float score_factor(const Params& p, int) { return p.a.scale_log2; }
   static __device__ __forceinline__ float value_factor(const Params&, int) { return 1.f; }
 };

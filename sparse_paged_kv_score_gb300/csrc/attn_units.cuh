@@ -6,6 +6,8 @@
 //   kPage           bytes of a page-head
 //   kCtaPages, kPartPages, kUnitPages, kEndPages   how pages are dealt, see below
 //   Params          the kernel's parameters: a (AttnParams), pool, parts, part_pages
+//   Held            what attend_units takes of them: a reference, or a copy (no call leaves the kernel, so that only the
+//                   compiler's choice of registers differs)
 //   Warp            a warp's arithmetic: reset(), load_q(), page() and store() as Softmax and the formats have them
 //   score_factor(p, h), value_factor(p, h)   of kv head h: queries' scores to log2 units, values
 #pragma once
@@ -254,7 +256,7 @@ __device__ __forceinline__ void write_row(const AttnParams& p, int64_t row, int 
 // (EITHER); or by unit without counting other units' pages (BY_UNIT).  (With EITHER alone for the first two 256 units
 // of 65 pages of a 4-bit cache take 0.5 us more.)
 template <class F, bool EITHER, bool BY_UNIT>
-__device__ __forceinline__ void attend_units(const typename F::Params& pf) {
+__device__ __forceinline__ void attend_units(typename F::Held pf) {
   using C = F;
   constexpr int TEAMS = C::TEAMS, NS = C::NS, L = C::L;
   extern __shared__ __align__(128) uint8_t smem_raw[];
