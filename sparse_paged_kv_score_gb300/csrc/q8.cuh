@@ -3,6 +3,9 @@
 // magnitude of the sub-block's rows and E = floor(log2 a):  s = 2^(E - 6), at least 2^-126; 0 for a = 0, NaN where a
 // value is not finite.
 //   - |value - x| <= s / 2 <= a / 128, for every x of the sub-block.
+//   - The mean of value - x is 0 for numbers anywhere between two codes.  bf16 numbers of at least s lie g apart, s / g of them to
+//     a code: floors are taken of 0, g, .. s - g beyond it, (s - g) / 2 on average, so they come back g / 2 high, whatever their sign.
+//     N(0, 1) rows in bf16: +0.0022 in the mean beside an error of 0.0105 rms; in fp32 3e-6.
 //   - Floors compose: floor(floor(x / s) / 2^k) = floor(x / (2^k s)).  A sub-block whose scale grows as rows are added
 //     holds what it would hold had they all come at once, so appends may be cut into calls in any way.
 //   - (c + 1/2) s = (2 c + 1) s / 2 has 8 significant bits: exact in bf16, and 16 of them sum exactly in fp32.
