@@ -236,17 +236,17 @@ int paged_kv_unpack_q4(spkv_cache_t cache, const int32_t* pages, int n_pages, vo
 /* A cache held in 8 bits.  A sub-block's 16 tokens x 128 dims of one head share one scale, a power of two, keys and
  * values apart.  With a the largest magnitude of the rows that it holds and E = floor(log2 a) it holds
  *   s = 2^(E - 6), at least 2^-126;  code c = floor(x / s), -128 .. 127;  value = (c + 1/2) s
- * so a value is off by at most s / 2 <= a / 128: 8.02 bits a value, 16416 bytes a page-head (bf16: 32768).  In the mean
- * nothing is added to numbers that lie anywhere between two codes (rotated keys, which come in fp32).  Numbers in bf16
- * (values, keys appended as they are) lie on steps of their own, g = 2^-8 to 2^-7 of their magnitude, s / g of them to a
- * code: those of at least s are read back g / 2 too high on average, positive and negative ones alike, and zero as s / 2.
- * A weighted mean of many bf16 values therefore comes out half a bf16 step of theirs high, where the rest of the error,
- * of either sign, averages out.  A sub-block of
- * zeros has the scale 0 and holds zeros; one with an infinity or a NaN has a NaN scale and reads back as NaN until its page
- * is begun again.  Rows that are added to a sub-block can only raise its scale; its codes are then floored again, which
- * leaves what they would be had all rows come at once: however appends are cut into calls, the cache holds the same.  (Where
- * rows are overwritten while their sub-block holds others, its scale stays at least what it was.)  Values are exact in bf16,
- * sub-block sums in fp32.
+ * so a value is off by at most s / 2, which is a / 128 at most (2^-127 where a < 2^-120): 8.02 bits a value, 16416
+ * bytes a page-head (bf16: 32768).  In the mean nothing is added to numbers that lie anywhere between two codes
+ * (rotated keys, which come in fp32).  Numbers in bf16 (values, keys appended as they are) lie on steps of their own,
+ * g = 2^-8 to 2^-7 of their magnitude, s / g of them to a code: those of at least s are read back g / 2 too high on
+ * average, positive and negative ones alike, and zero as s / 2.  A weighted mean of many bf16 values therefore comes
+ * out half a bf16 step of theirs high, where the rest of the error, of either sign, averages out.  A sub-block of
+ * zeros has the scale 0 and holds zeros; one with an infinity or a NaN has a NaN scale and reads back as NaN until
+ * its page is begun again.  Rows that are added to a sub-block can only raise its scale; its codes are then floored
+ * again, which leaves what they would be had all rows come at once: however appends are cut into calls, the cache
+ * holds the same.  (Where rows are overwritten while their sub-block holds others, its scale stays at least what it
+ * was.)  Values are exact in bf16, sub-block sums in fp32.
  *   kv_pool : [n_kv_heads][n_phys_pages][16416] bytes, 16-byte aligned.  Inside a page-head, with t the token, d the dim and
  *             u = c + 128 the byte of a code:
  *     key codes    1024 (t / 8) + 512 ((d / 16) % 2) + 64 (t % 8) + 16 (d / 32) + d % 16

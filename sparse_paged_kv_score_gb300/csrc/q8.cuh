@@ -2,7 +2,7 @@
 // two, and a byte u = c + 128 for a value (c + 1/2) s with the code c = floor(x / s) in [-128, 127].  With a the largest
 // magnitude of the sub-block's rows and E = floor(log2 a):  s = 2^(E - 6), at least 2^-126; 0 for a = 0, NaN where a
 // value is not finite.
-//   - |value - x| <= s / 2 <= a / 128, for every x of the sub-block.
+//   - |value - x| <= s / 2 <= max(a / 128, 2^-127), for every x of the sub-block.
 //   - The mean of value - x is 0 for numbers anywhere between two codes.  bf16 numbers of at least s lie g apart, s / g of them to
 //     a code: floors are taken of 0, g, .. s - g beyond it, (s - g) / 2 on average, so they come back g / 2 high, whatever their sign.
 //     N(0, 1) rows in bf16: +0.0022 in the mean beside an error of 0.0105 rms; in fp32 3e-6.

@@ -35,3 +35,12 @@ def test_numbers_anywhere_between_the_codes_keep_their_mean():
     x = rng.uniform(-1.9, 1.9, n).astype(np.float32).astype(np.float64)
     error = read_back(x, s) - x
     assert abs(error.mean()) <= 5 * s / np.sqrt(12 * n) + 2.0 ** -17 * s
+
+
+@pytest.mark.parametrize("e", [-149, -133, -127, -126, -121, -120, -119, 0, 127])
+def test_largest_error_of_a_block(e):
+    """s / 2 for a block whose largest magnitude a has the exponent e: a / 128 at most, but 2^-127 where a is below 2^-120."""
+    s = np.float64(ref.scale_of(2.0 ** e))
+    x = np.append(np.random.default_rng(2).uniform(-2.0 ** e, 2.0 ** e, 1000), [2.0 ** e, -2.0 ** e, 0.0])
+    assert np.abs(read_back(x, s) - x).max() <= s / 2
+    assert s / 2 <= max(2.0 ** e / 128, 2.0 ** -127) and (s / 2 <= 2.0 ** e / 128) == (e >= -120)
