@@ -10,8 +10,9 @@
 // K groups, K of their lines and K elements, of equal ones the first each time (an element among the K best lies in a line
 // whose maximum is among the K best of the lines', as each line ahead of it holds an element ahead of it, and likewise a line
 // in its group; groups, lines and elements are numbered by beam and token).
-// Sums are fp32 within 4 KiB, and over a row's groups, a 32nd of them to a lane.  Scores have 48 bits: those of different beams
-// may lie close together.
+// Sums are fp32 within 4 KiB, and over a row's groups, a 32nd of them to a lane: a beam's lse is off by up to 7.7e-6 at 128256 tokens (spkv.h
+// has the bound), and so is the order of different beams.  What is added to it has 48 bits, so that a large cum takes nothing
+// from the order of a beam's own tokens and rows that are alike tie.
 //
 // beam_reorder.  Complete pages are shared, so a child takes its parent's table entries; of the part-filled page a parent's
 // first child keeps the parent's own, and each other child gets the page of a beam without children, with the parent's rows
