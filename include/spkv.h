@@ -299,7 +299,8 @@ int beam_plan_destroy(spkv_beam_plan_t plan);
  *   tokens, parents, scores : device int32, int32, fp32 [B][K]; where there are fewer than K candidates -1, -1, -infinity
  * A logit of -infinity is no candidate (masks may use it, or their type's lowest value).  A beam whose logits or score hold a
  * NaN or +infinity has no candidates (SPKV_DEVERR_BEAM).  K may be larger than W, for callers that take the ended ones out;
- * W <= 64, K <= 128, W rows of at most 2^27 bytes together (else SPKV_EUNSUPPORTED). */
+ * W <= 64, K <= 128, W times a row's bytes rounded up to a multiple of 4096 at most 2^27, and B * W rows of these at most
+ * 2^42 (else SPKV_EUNSUPPORTED). */
 int beam_select(spkv_cache_t cache, spkv_beam_plan_t plan, const void* logits, int type, int64_t row_stride, int B, int W,
                 int V, const float* cum, int K, int32_t* tokens, int32_t* parents, float* scores, void* stream);
 
