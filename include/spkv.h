@@ -275,7 +275,8 @@ int paged_kv_create_q8(const spkv_desc_q8* desc, void* stream, spkv_cache_t* out
 int paged_kv_unpack_q8(spkv_cache_t cache, const int32_t* pages, int n_pages, void* k_out, void* v_out, void* stream);
 
 /* Beam search over a paged cache: a decode step of B requests with W beams each is a step of B * W sequences (row
- * b * W + w of every tensor is beam w of request b), then beam_select on its logits and beam_reorder. */
+ * b * W + w of every tensor is beam w of request b), then beam_select on its logits and beam_reorder.  beam_select touches no
+ * page: of the handle it takes the device and the error word, and any handle of the device will do. */
 
 enum spkv_dtype { SPKV_F32 = 0, SPKV_BF16 = 1, SPKV_F16 = 2 };
 
@@ -314,11 +315,15 @@ int beam_select(spkv_cache_t cache, spkv_beam_plan_t plan, const void* logits, i
  * Before the first step, with the prompt in beam 0's pages and a page of its own in column L / 64 of every beam, parents of 0
  * make all beams continue it.  Pages that no table names any more are the caller's to find (complete pages only: none is lost
  * from column L / 64).  Any cache format; handles without summaries or page_cnt have whole pages copied.
+ * Flat page tables only: a two-level directory (spkv_page_dir) and what a handle's user keeps for each beam beside its table
+ * (resident slots and their lists, alive pages, recency) do not follow the parents; a caller who keeps such state moves it by
+ * `parents` himself.
  *   parents    : device int32 [B][W];  seq_len: device int32 [B W]
  *   page_table : device int32 [B W][np_max], changed in place
  * A request with a parent outside [-1, W) or beams of different lengths is left as it is (SPKV_DEVERR_BEAM), one with column
  * L / 64 outside the table too (SPKV_DEVERR_PAGE_ID); a copy from or to a page outside the pool is left out
- * (SPKV_DEVERR_PHYS).  W <= 64 (else SPKV_EUNSUPPORTED), B * W * n_kv_heads <= max_units. */
+ * (SPKV_DEVERR_PHYS).  W <= 64 (else SPKV_EUNSUPPORTED), B * W * n_kv_heads <= max_units, as for the attention over the same
+ * beams. */
 int beam_reorder(spkv_cache_t cache, const int32_t* parents, int B, int W, int32_t* page_table, int np_max,
                  const int32_t* seq_len, void* stream);
 

@@ -402,7 +402,8 @@ def beam_select(cache: PagedKVCache, plan: BeamPlan, logits, cum, tokens, parent
 def beam_reorder(cache: PagedKVCache, parents, page_table, seq_len, stream=None):
     """Beam w of request b continues parents[b][w] (int32 [B][W], -1: it stops): its row b W + w of page_table (int32
     [B W][np_max]) gets the parent's complete pages, and where the parent's last page is part-filled and another child keeps
-    it, a page of its own with the parent's rows.  seq_len int32 [B W]: the tokens in the beams, alike in a request."""
+    it, a page of its own with the parent's rows.  seq_len int32 [B W]: the tokens in the beams, alike in a request.
+    Flat tables only: a PageMap's directory, resident slots and their lists do not follow."""
     B, W = parents.shape
     np_max = page_table.shape[1]
     dev = cache.tensors[0].get_device()
