@@ -143,10 +143,11 @@ __global__ void __launch_bounds__(128, 4) append_q8_rows_kernel(const __grid_con
     vx = *reinterpret_cast<const uint4*>(v_new + r * p.v_stride);
   };
   if (hw < own) load(hw);
+  const uint16_t* const q = q_row(p, h, base + rq, sub);
   if (rq < own) {
 #pragma unroll
     for (int k = 0; k < kHeads; ++k)
-      if (sub + k * step < p.G) qv[k] = load_pairs(q_row(p, h, base + rq, sub + k * step), l);
+      if (sub + k * step < p.G) qv[k] = load_pairs(q + k * step * kHeadDim, l);
   }
   if (tid < 2 * kMaxWindow) S.top[tid >> 1][tid & 1] = 0;
   if (warp == 0) {
@@ -236,7 +237,7 @@ __global__ void __launch_bounds__(128, 4) append_q8_rows_kernel(const __grid_con
   // ---- query heads
   if (rq < own && sub < p.G && info[rq].rot) {
     CosSin u;
-    turn_queries(p, h, base + rq, axis_pos[rq], sub, step, l, qv, u);
+    turn_queries(p, h, base + rq, axis_pos[rq], sub, step, l, q, qv, u);
   }
   // ---- rows rotated into shared memory, their sub-blocks' largest magnitudes
 #pragma unroll

@@ -65,10 +65,11 @@ __global__ void __launch_bounds__(256, 4) append_rope_kernel(const __grid_consta
     kx = load_pairs(k_new + hw * p.k_stride, l);
     vx = *reinterpret_cast<const uint4*>(v_new + hw * p.v_stride);
   }
+  const uint16_t* const q = q_row(p, h, base + rq, sub);
   if (rq < own) {
 #pragma unroll
     for (int k = 0; k < kHeads; ++k)
-      if (sub + k * step < p.G) qv[k] = load_pairs(q_row(p, h, base + rq, sub + k * step), l);
+      if (sub + k * step < p.G) qv[k] = load_pairs(q + k * step * kHeadDim, l);
   }
   if (warp == 0) {
     uint32_t bad = 0;
@@ -83,7 +84,7 @@ __global__ void __launch_bounds__(256, 4) append_rope_kernel(const __grid_consta
 
   // ---- query heads
   CosSin t{};
-  if (rq < own && sub < p.G && info[rq].rot) turn_queries(p, h, base + rq, axis_pos[rq], sub, step, l, qv, t);
+  if (rq < own && sub < p.G && info[rq].rot) turn_queries(p, h, base + rq, axis_pos[rq], sub, step, l, q, qv, t);
   // ---- keys and values of the window's sub-blocks
   for (int r = hw; r < n_hw * ((kMaxRows + n_hw - 1) / n_hw); r += n_hw) {
     const RowInfo ri = info[min(r, 31)];
