@@ -15,9 +15,10 @@
 //
 // Measured (GB300, from a replayed graph): 32 rows of a decode batch, 32 + 2 x 8 heads 5.7 us, latency: lengths, page table,
 // what the page holds, read one after the other between three barriers; 6000 rows of four prompts 31.7 us = 139 MB at 4.4 TB/s
-// (0.66 of the copy rate; to bf16 pages 31), 20000 rows 96 us = 4.8 TB/s; their keys and values alone 17.5 of 31.7.  With a CTA
-// a window and head for many rows too (rows through shared memory, a barrier for the largest magnitudes and one for the
-// bytes) those took 42 and 134 us: 600 instructions a warp for two rows, and every phase as long as its slowest warp.
+// (0.66 of the copy rate; to bf16 pages 31), 20000 rows 96 us = 4.8 TB/s; the 6000 without queries 22.7, as one prompt from
+// its first token 17.6 of 30.9.  With a CTA a window and head for many rows too (rows through shared memory, a barrier for
+// the largest magnitudes and one for the bytes) 6000 and 20000 rows took 42 and 134 us: 600 instructions a warp for two
+// rows, and every phase as long as its slowest warp.
 #include "append_rope.cuh"
 #include "q8.cuh"
 

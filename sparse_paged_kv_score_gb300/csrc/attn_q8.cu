@@ -403,10 +403,12 @@ struct Units8 : Shape8<HEADS> {
 };
 
 // Measured (GB300, from a replayed graph): 256 units of 65 pages, 4 heads 50.1 us = 275 MB at 5.5 TB/s (0.82 of the copy rate);
-// 8 heads 49.0, 16 heads 60.2; 61 lists of up to 129 pages, 16 heads 26 us; 2 of 17 pages 6.4.  Times of 96 to 300 units lie on
+// 8 heads 49.1, 16 heads 60.2; 61 lists of up to 129 pages, 16 heads 26 us; 2 of 17 pages 6.4.  Times of 96 to 300 units lie on
 // a line of 6.37 TB/s (0.95 of the copy rate) behind 8 us: lengths, lists, page table and first page read one after the
-// other, and the CTAs' ends.  With 9 to 16 heads a page's 1240 instructions in two warps are what bounds it, in chains that two
-// warps a scheduler (255 registers) do not hide: they issue in a third of the slots.
+// other, and the CTAs' ends.  The 61 ragged lists (4138 pages, 9.8 us of bytes) take 19.4 us with 4 heads and 20.7 with 8, so 10 us and
+// more of the 26 with 16 are not the heads'.  A page is 1000, 1030, 1300 instructions of its two warps together (4, 8, 16 heads) and a CTA's start,
+// ends and merges 6400, 6600, 9100 beside its pages: a third of the ragged case's 8.2 million with 16 heads.  The
+// rest of those is chains that two warps a scheduler (255 registers) do not hide: a third of the slots issue.
 enum Mode { kDealt, kEither, kByUnit };
 
 template <int HEADS, Mode MODE>

@@ -46,8 +46,8 @@ __device__ __forceinline__ uint32_t open2(uint32_t f16, float s) {
 
 // One CTA per (listed page, head).  Keys: a thread takes 8 dims of a token, 8 bytes in and 16 out, so that half a warp's
 // store is a row.  Values: 8 dims of two tokens, 16 bytes in and 16 out for each.
-// Bound by HBM: 2048 pages of 8 heads, 0.95 of their rows there, 117 us = 705 MB that move at 6.0 TB/s (with the last writes
-// still in L2; 0.99 of the floor of all rows); 17 pages of 2 heads 2.9 us, a launch and two reads one after the other.
+// Bound by HBM: 2048 pages of 8 heads, 0.95 of their rows there (766 MB), 121 us from a replayed graph = 6.3 TB/s (0.94 of the copy
+// rate); 17 pages of 2 heads 2.9 us, a launch and two reads one after the other.
 __global__ void __launch_bounds__(256)
     unpack_q8_kernel(const uint8_t* __restrict__ pool, const int32_t* __restrict__ page_cnt, const int32_t* __restrict__ pages,
                      int n_pages, int64_t n_phys, uint4* __restrict__ k_out, uint4* __restrict__ v_out, uint32_t* err) {
