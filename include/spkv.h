@@ -268,7 +268,8 @@ typedef struct {
 
 /* paged_kv_create for an 8-bit cache.  What paged_kv_create_q4 says of a 4-bit handle holds for this one: which calls work
  * on it (paged_kv_unpack_q8 for paged_kv_unpack_q4) and which refuse it, slots (16416 bytes a page's head), devices and the
- * attention's limits. */
+ * attention's limits.  Its sums of weighted values stay in fp32's range while N tokens that are attended together have
+ * magnitudes up to 2^113 / N. */
 int paged_kv_create_q8(const spkv_desc_q8* desc, void* stream, spkv_cache_t* out);
 
 /* paged_kv_unpack_q4 for an 8-bit cache; the values are exact. */

@@ -10,7 +10,8 @@
 //
 // The products run on mma.sync m16n8k16 in f16 with fp32 accumulators, keys (then value dims) as M and the query heads
 // as N: f16 holds a code exactly, a query row is scaled into f16 as the 4-bit attention's are (attn_units.cuh), the
-// weights are split into f16 hi + lo parts (22 bits).
+// weights are split into f16 hi + lo parts (22 bits).  They are below 2^15 (attn_units.cuh) and meet sv in fp32, so sums over N tokens stay
+// in range for values up to 2^113 / N.
 #include "attn_units.cuh"
 #include "q8.cuh"
 
